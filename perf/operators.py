@@ -116,8 +116,9 @@ def draw(rng):
         else:
             c = _attend("", seqs, new_lo, new_hi, past_lo, past_hi, hq, hkv, dim, page, rng.choice(["f16", "bf16"]),
                         single, rng.choice([0, 0, 0, _log(rng, 1, 4096)]), rng.random() < 0.3)
-        # no more bytes, and no more (query, key) pairs, than the largest listed cases have
-        while c["seqs"] > 1 and work(c)["bytes"] > 64 * 4096 * 8 * 2 * 128:
+        # no more bytes, cached keys and (query, key) pairs than the largest listed cases have
+        keys = 64 * 8192 * 8 * 128
+        while c["seqs"] > 1 and (work(c)["bytes"] > keys or c["seqs"] * (c["new_hi"] + c["past_hi"]) * c["hkv"] * c["dim"] > keys):
             c["seqs"] -= 1
         while op == "attend" and c["seqs"] * c["new_hi"] * (c["new_hi"] + c["past_hi"]) * c["hq"] > 8192 * 8192 * 16:
             c["seqs"], c["new_hi"] = max(1, c["seqs"] // 2), max(2 - c["single"], c["new_hi"] // 2)
