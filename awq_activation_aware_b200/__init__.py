@@ -14,12 +14,17 @@ from pathlib import Path
 
 import torch
 
+from . import kv
+from .kv import (attention_step, kv_append, kv_attention, kv_attention_workspace_bytes, kv_cache, rope,  # noqa: F401
+                 rope_table)
+
 __all__ = [
     "AWQError", "lib", "act_stats", "alpha_scales", "quant_dequant", "search_workspace_bytes",
     "search_layer", "pack", "quantize_layer", "get_status", "set_wait_timeout_ms", "default_alphas",
     "profile_next_search", "quantize_shared_input", "selftest_bounded_wait", "qlinear",
     "search_scales", "channel_topk", "pack_scales", "salient_scales", "baselines", "output_error",
     "gptq_hessian", "gptq_factor", "gptq_quantize", "gptq_layer", "awq_gptq", "LIB_PATH",
+    "rope_table", "rope", "kv_cache", "kv_append", "kv_attention", "kv_attention_workspace_bytes", "attention_step",
 ]
 
 _PKG = Path(__file__).resolve().parent
@@ -100,6 +105,7 @@ def lib():
                "awq_gptq_hessian_tc", "awq_gptq_factor",
                "awq_gptq_quantize", "awq_qlinear_tc", "awq_qlinear_cc"):
         getattr(L, fn).restype = ctypes.c_int
+    kv.declare(L)
     _lib = L
     return L
 

@@ -17,7 +17,8 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libawq.so"
 SOURCES = [CSRC / "awq_abi.cu"]
-DEPS = SOURCES + [CSRC / "awq_kernels.cuh", CSRC / "awq_device.cuh", ROOT / "include" / "awq.h"]
+DEPS = SOURCES + [CSRC / "awq_kernels.cuh", CSRC / "awq_device.cuh", CSRC / "awq_kv.cuh",
+                  CSRC / "awq_kv_abi.cuh", ROOT / "include" / "awq.h"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",

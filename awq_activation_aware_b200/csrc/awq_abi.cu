@@ -6,12 +6,14 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
 
 #include "awq.h"
 #include "awq_kernels.cuh"
+#include "awq_kv.cuh"
 
 namespace {
 
@@ -1002,9 +1004,11 @@ awq_status awq_get_status(void *stream) {
         const unsigned zero = 0;
         if (cudaMemcpyToSymbol(awq::g_dev_error, &zero, sizeof(zero)) != cudaSuccess) return AWQ_ERR_CUDA;
         if (flags & awq::kDevErrTimeout) return AWQ_ERR_TIMEOUT;
-        if (flags & (awq::kDevErrBadAlpha | awq::kDevErrBadScale | awq::kDevErrNotPD)) return AWQ_ERR_INVALID_ARG;
+        if (flags & (awq::kDevErrBadAlpha | awq::kDevErrBadScale | awq::kDevErrNotPD | awq::kv::kDevErrBadIndex)) return AWQ_ERR_INVALID_ARG;
     }
     return last_launch();
 }
 
 }  // extern "C"
+
+#include "awq_kv_abi.cuh"

@@ -1,0 +1,254 @@
+// Host side of the cache operators of include/awq.h: argument checks, workspace
+// layout and launches.  Included by awq_abi.cu after its helpers.
+#pragma once
+
+namespace {
+
+bool kv_dtype_ok(int t) { return t >= AWQ_F32 && t <= AWQ_BF16; }
+
+// Rows whose accesses may be 16 bytes wide: aligned base, strides of whole
+// 8-element groups.
+bool kv_rows_aligned(const awq_rows &r) {
+    return aligned16(r.data) && r.token_stride % 8 == 0 && r.head_stride % 8 == 0;
+}
+// Element-aligned base of a known type.
+bool kv_rows_base(const awq_rows &r) {
+    return r.data && kv_dtype_ok(r.dtype) && reinterpret_cast<uintptr_t>(r.data) % (r.dtype == AWQ_F32 ? 4 : 2) == 0;
+}
+bool kv_rows_in(const awq_rows &r) {
+    return kv_rows_base(r) && r.heads >= 1 && r.token_stride >= 0 && r.head_stride >= 0;
+}
+// Written rows must not overlap: heads inside a token, or tokens inside a head.
+bool kv_rows_out(const awq_rows &r, int64_t T, int64_t D) {
+    if (!kv_rows_base(r) || r.heads < 1 || r.head_stride < D || r.token_stride < D) return false;
+    if (r.heads == 1 || T == 1) return true;
+    return r.token_stride >= (r.heads - 1) * r.head_stride + D || r.head_stride >= (T - 1) * r.token_stride + D;
+}
+awq::kv::Rows kv_rows(const awq_rows &r) { return {r.data, r.token_stride, r.head_stride, r.heads, r.dtype}; }
+
+bool kv_cache_ok(const awq_kv_cache &c) {
+    if (!c.k_codes || !c.v_codes || !c.k_scales || !c.v_scales || !aligned16(c.k_codes) || !aligned16(c.v_codes) ||
+        !aligned16(c.k_scales) || !aligned16(c.v_scales))
+        return false;
+    if (c.page_size != 16 && c.page_size != 32 && c.page_size != 64 && c.page_size != 128 && c.page_size != 256)
+        return false;
+    if (c.head_dim != 64 && c.head_dim != 128) return false;
+    // rows of all pages are addressed by a 32-bit tensor coordinate
+    return c.heads >= 1 && c.heads <= 1024 && c.n_pages >= 1 &&
+           c.n_pages <= kMaxDim / ((int64_t)c.heads * c.page_size);
+}
+awq::kv::Cache kv_cache(const awq_kv_cache &c) {
+    awq::kv::Cache k;
+    k.codes[0] = static_cast<uint8_t *>(c.k_codes);
+    k.codes[1] = static_cast<uint8_t *>(c.v_codes);
+    k.scales[0] = c.k_scales;
+    k.scales[1] = c.v_scales;
+    k.n_pages = c.n_pages;
+    k.page = c.page_size;
+    k.heads = c.heads;
+    k.dim = c.head_dim;
+    return k;
+}
+bool kv_batch_ok(const awq_kv_batch &b, int64_t T) {
+    if (!b.seq_lens || !b.pages || b.n_seqs < 1 || b.n_seqs > (1 << 20) || b.max_pages < 1 || b.max_pages > kMaxDim ||
+        b.page_stride < b.max_pages)
+        return false;
+    return T >= 1 && T <= kMaxDim && (b.cu_tokens || T == b.n_seqs);
+}
+awq::kv::Batch kv_batch(const awq_kv_batch &b) {
+    return {b.seq_lens, b.cu_tokens, b.pages, b.page_stride, b.max_pages, (int)b.n_seqs};
+}
+// A table for rotations of the first rot_dim of D elements.
+bool kv_rope_ok(const awq_rope_cfg &r, int64_t D) {
+    return r.table && aligned16(r.table) && r.n_pos >= 1 && r.n_pos <= kMaxDim && r.rot_dim >= 2 && r.rot_dim <= D &&
+           r.rot_dim % 2 == 0 && (r.layout == AWQ_ROPE_HALF || r.layout == AWQ_ROPE_INTERLEAVED);
+}
+awq::kv::Rope kv_rope(const awq_rope_cfg &r) {
+    return {reinterpret_cast<const float2 *>(r.table), r.n_pos, r.rot_dim, r.layout == AWQ_ROPE_INTERLEAVED};
+}
+
+template <typename TI, typename TO>
+void launch_rope(const awq::kv::RopeArgs &A, int64_t T, bool vec, cudaStream_t st) {
+    const int64_t items = (int64_t)A.x.heads * (vec ? awq::kv::rope_items(A.dim, A.r.rot, A.r.interleaved) : A.dim / 2);
+    const int threads = items >= 256 ? 256 : (int)((items + 31) / 32 * 32);
+    if (vec) awq::kv::rope_kernel<TI, TO, true><<<(unsigned)T, threads, 0, st>>>(A);
+    else awq::kv::rope_kernel<TI, TO, false><<<(unsigned)T, threads, 0, st>>>(A);
+}
+template <typename TI>
+void launch_rope_to(const awq::kv::RopeArgs &A, int64_t T, bool vec, cudaStream_t st) {
+    if (A.y.dtype == awq::kv::kF32) launch_rope<TI, float>(A, T, vec, st);
+    else if (A.y.dtype == awq::kv::kF16) launch_rope<TI, __half>(A, T, vec, st);
+    else launch_rope<TI, __nv_bfloat16>(A, T, vec, st);
+}
+
+template <typename TI, typename TO>
+void launch_append_dim(const awq::kv::AppendArgs &A, dim3 grid, cudaStream_t st) {
+    if (A.C.dim == 64) awq::kv::kv_append_kernel<TI, TO, 64><<<grid, awq::kv::kAppendThreads, 0, st>>>(A);
+    else awq::kv::kv_append_kernel<TI, TO, 128><<<grid, awq::kv::kAppendThreads, 0, st>>>(A);
+}
+template <typename TI>
+void launch_append(const awq::kv::AppendArgs &A, dim3 grid, cudaStream_t st) {
+    if (A.q_out.dtype == awq::kv::kF32) launch_append_dim<TI, float>(A, grid, st);
+    else if (A.q_out.dtype == awq::kv::kF16) launch_append_dim<TI, __half>(A, grid, st);
+    else launch_append_dim<TI, __nv_bfloat16>(A, grid, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+awq_status awq_rope_table(int64_t n_pos, int32_t rot_dim, double base, awq_rope_scaling sc, float *table,
+                          void *stream) {
+    if (!table || !aligned16(table) || n_pos < 1 || n_pos > kMaxDim || rot_dim < 2 || rot_dim % 2 || rot_dim > 65536 ||
+        !(base > 1.0 && base <= 1e12))
+        return AWQ_ERR_INVALID_ARG;
+    if (sc.kind < AWQ_ROPE_PLAIN || sc.kind > AWQ_ROPE_YARN) return AWQ_ERR_INVALID_ARG;
+    if (sc.kind != AWQ_ROPE_PLAIN && !(sc.factor >= 1.0 && sc.factor <= 1e6)) return AWQ_ERR_INVALID_ARG;
+    if (sc.kind == AWQ_ROPE_NTK && rot_dim < 4) return AWQ_ERR_INVALID_ARG;
+    awq::kv::TableArgs A;
+    A.table = reinterpret_cast<float2 *>(table);
+    A.n_pos = n_pos;
+    A.half = rot_dim / 2;
+    A.log_base = std::log(base);
+    A.inv_factor = 1.0;
+    A.ramp_lo = 0.0;
+    A.ramp_hi = 1.0;
+    A.magnitude = 1.0;
+    if (sc.kind == AWQ_ROPE_LINEAR) {
+        A.inv_factor = 1.0 / sc.factor;
+        A.ramp_lo = -1.0;                      // every pair past the ramp
+        A.ramp_hi = 0.0;
+    } else if (sc.kind == AWQ_ROPE_NTK) {
+        A.log_base += std::log(sc.factor) * rot_dim / (rot_dim - 2);
+    } else if (sc.kind == AWQ_ROPE_YARN) {
+        if (!(sc.original >= 1.0 && sc.original <= 1e12) || !(sc.beta_fast > 0.0 && sc.beta_fast <= 1e6) ||
+            !(sc.beta_slow > 0.0 && sc.beta_slow <= sc.beta_fast) || !(sc.magnitude >= 0.0 && sc.magnitude <= 1e6))
+            return AWQ_ERR_INVALID_ARG;
+        const double two_pi = 6.283185307179586;
+        const double lo = std::floor(rot_dim * std::log(sc.original / (sc.beta_fast * two_pi)) / (2.0 * A.log_base));
+        const double hi = std::ceil(rot_dim * std::log(sc.original / (sc.beta_slow * two_pi)) / (2.0 * A.log_base));
+        A.inv_factor = 1.0 / sc.factor;
+        A.ramp_lo = lo > 0.0 ? lo : 0.0;
+        A.ramp_hi = hi < rot_dim - 1 ? hi : rot_dim - 1;
+        if (A.ramp_hi - A.ramp_lo < 0.001) A.ramp_hi = A.ramp_lo + 0.001;
+        A.magnitude = sc.magnitude > 0.0 ? sc.magnitude : 0.1 * std::log(sc.factor) + 1.0;
+    }
+    DevInfo d;
+    if (awq_status e = device_info(d)) return e;
+    int grid = blocks_for(n_pos * A.half, 256);
+    if (grid > 16 * d.sms) grid = 16 * d.sms;
+    awq::kv::rope_table_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(A);
+    return last_launch();
+}
+
+awq_status awq_rope(awq_rows x, awq_rows y, int64_t T, int32_t head_dim, const int32_t *positions, awq_rope_cfg r,
+                    int32_t inverse, void *stream) {
+    if (T < 1 || T > kMaxDim || head_dim < 2 || head_dim % 2 || head_dim > 65536 || !positions ||
+        (inverse != 0 && inverse != 1) || !kv_rope_ok(r, head_dim) || !kv_rows_in(x) || !kv_rows_out(y, T, head_dim) ||
+        x.heads != y.heads)
+        return AWQ_ERR_INVALID_ARG;
+    // in place: element for element the same memory, or another array altogether
+    if (x.data == y.data &&
+        (x.dtype != y.dtype || x.token_stride != y.token_stride || x.head_stride != y.head_stride))
+        return AWQ_ERR_INVALID_ARG;
+    DevInfo d;
+    if (awq_status e = device_info(d)) return e;
+    awq::kv::RopeArgs A;
+    A.x = kv_rows(x);
+    A.y = kv_rows(y);
+    A.dim = head_dim;
+    A.inverse = inverse;
+    A.positions = positions;
+    A.r = kv_rope(r);
+    const bool vec = kv_rows_aligned(x) && kv_rows_aligned(y) && head_dim % 8 == 0 &&
+                     r.rot_dim % (A.r.interleaved ? 8 : 16) == 0;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (x.dtype == AWQ_F32) launch_rope_to<float>(A, T, vec, st);
+    else if (x.dtype == AWQ_F16) launch_rope_to<__half>(A, T, vec, st);
+    else launch_rope_to<__nv_bfloat16>(A, T, vec, st);
+    return last_launch();
+}
+
+awq_status awq_kv_append(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows k, awq_rows v, awq_rows q, awq_rows q_out,
+                         awq_rope_cfg r, void *stream) {
+    if (!kv_cache_ok(c) || !kv_batch_ok(b, T)) return AWQ_ERR_INVALID_ARG;
+    if (!kv_rows_in(k) || !kv_rows_in(v) || !kv_rows_aligned(k) || !kv_rows_aligned(v) || k.dtype != v.dtype ||
+        k.heads != c.heads || v.heads != c.heads)
+        return AWQ_ERR_INVALID_ARG;
+    if (r.table && !kv_rope_ok(r, c.head_dim)) return AWQ_ERR_INVALID_ARG;
+    if (q.data) {
+        if (!r.table || !kv_rows_in(q) || !kv_rows_out(q_out, T, c.head_dim) || !kv_rows_aligned(q) ||
+            !kv_rows_aligned(q_out) || q.dtype != k.dtype || q.heads != q_out.heads || q.heads > 65536)
+            return AWQ_ERR_INVALID_ARG;
+        if (q.data == q_out.data && (q.dtype != q_out.dtype || q.token_stride != q_out.token_stride ||
+                                     q.head_stride != q_out.head_stride))
+            return AWQ_ERR_INVALID_ARG;
+    }
+    DevInfo d;
+    if (awq_status e = device_info(d)) return e;
+    awq::kv::AppendArgs A;
+    A.C = kv_cache(c);
+    A.B = kv_batch(b);
+    A.T = T;
+    A.kv[0] = kv_rows(k);
+    A.kv[1] = kv_rows(v);
+    A.q = kv_rows(q);
+    A.q_out = kv_rows(q.data ? q_out : k);
+    A.r = r.table ? kv_rope(r) : awq::kv::Rope{nullptr, 0, 0, 0};
+    A.chunk = b.cu_tokens ? 16 : 1;
+    A.chunks = (T + A.chunk - 1) / A.chunk;
+    const int64_t blocks = A.chunks + (q.data ? T : 0);
+    if (blocks > kMaxDim) return AWQ_ERR_INVALID_ARG;
+    // several blocks share a chunk while the machine is not full
+    int gy = 1;
+    while (gy * 2 * 8 <= 2 * c.heads * A.chunk && blocks * gy < 4 * d.sms) gy *= 2;
+    const dim3 grid((unsigned)blocks, (unsigned)gy);
+    cudaStream_t st = (cudaStream_t)stream;
+    if (k.dtype == AWQ_F32) launch_append<float>(A, grid, st);
+    else if (k.dtype == AWQ_F16) launch_append<__half>(A, grid, st);
+    else launch_append<__nv_bfloat16>(A, grid, st);
+    return last_launch();
+}
+
+size_t awq_kv_attention_workspace_bytes(awq_kv_cache c, int64_t T, int32_t q_heads, int32_t max_tokens) {
+    (void)c; (void)T; (void)q_heads; (void)max_tokens;
+    return 256;
+}
+
+awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows q, awq_rows out, float scale,
+                            int32_t max_tokens, int64_t window, float *lse, void *ws, size_t ws_bytes, void *stream) {
+    if (!kv_cache_ok(c) || !kv_batch_ok(b, T)) return AWQ_ERR_INVALID_ARG;
+    if (!kv_rows_in(q) || !kv_rows_out(out, T, c.head_dim) || !kv_rows_aligned(q) || !kv_rows_aligned(out) ||
+        (q.dtype != AWQ_F16 && q.dtype != AWQ_BF16) || out.dtype != q.dtype || q.heads != out.heads ||
+        q.heads % c.heads || q.heads > 65535 || out.data == q.data)
+        return AWQ_ERR_INVALID_ARG;
+    if (!(scale > 0.0f && scale <= 1e6f) || window < 0 || max_tokens < 1 || (!b.cu_tokens && max_tokens != 1))
+        return AWQ_ERR_INVALID_ARG;
+    if (!ws || ws_bytes < awq_kv_attention_workspace_bytes(c, T, q.heads, max_tokens) ||
+        (reinterpret_cast<uintptr_t>(ws) & 255u))
+        return AWQ_ERR_WORKSPACE;
+    DevInfo d;
+    if (awq_status e = device_info(d)) return e;
+    awq::kv::AttnArgs A;
+    A.C = kv_cache(c);
+    A.B = kv_batch(b);
+    A.T = T;
+    A.q = kv_rows(q);
+    A.out = kv_rows(out);
+    A.scale_log2 = scale * 1.4426950408889634f;
+    A.window = window;
+    A.lse = lse;
+    cudaStream_t st = (cudaStream_t)stream;
+    const dim3 grid((unsigned)T, (unsigned)q.heads);
+    const bool h = q.dtype == AWQ_F16;
+    if (c.head_dim == 64) {
+        if (h) awq::kv::attn_plain_kernel<__half, 64><<<grid, 128, 0, st>>>(A);
+        else awq::kv::attn_plain_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(A);
+    } else {
+        if (h) awq::kv::attn_plain_kernel<__half, 128><<<grid, 128, 0, st>>>(A);
+        else awq::kv::attn_plain_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(A);
+    }
+    return last_launch();
+}
+
+}  // extern "C"

@@ -330,8 +330,8 @@ AWQ_API awq_status awq_pack_scales(const void *W, int64_t N, int64_t K, const fl
 /* Synchronises `stream`, then reports (and clears) errors raised on the device
  * since the last call: AWQ_ERR_TIMEOUT if a kernel's bounded wait ran out,
  * AWQ_ERR_INVALID_ARG if a kernel saw an alpha outside [0, 1], a given scale
- * that is not positive and finite, or a Hessian that is not positive definite,
- * AWQ_ERR_CUDA for
+ * that is not positive and finite, a Hessian that is not positive definite, or
+ * a position or cache page outside its array, AWQ_ERR_CUDA for
  * a pending CUDA error.  AWQ_OK otherwise. */
 AWQ_API awq_status awq_get_status(void *stream);
 
@@ -390,6 +390,132 @@ AWQ_API awq_status awq_qlinear_tc(const uint32_t *codes, const void *scales, con
                                   const float *s_best, int64_t N, int64_t K, awq_qcfg q,
                                   const void *X, int64_t T, int64_t ldx, float *Y,
                                   void *ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Between a decode step's quantized projections: rotary positions, a paged 8-bit
+ * cache of keys and values, and the attention over it.  (The pages end at the
+ * quantized linear layer; these are the other operators its user's step needs.)
+ *
+ * Element types of rows, and rows [T][heads][head_dim] with contiguous elements
+ * (strides in elements).  Rows that are read may share memory (a stride of 0
+ * broadcasts); rows that are written may not.                                  */
+enum { AWQ_F32 = 0, AWQ_F16 = 1, AWQ_BF16 = 2 };
+typedef struct {
+    void *data;                /* device */
+    int64_t token_stride, head_stride;
+    int32_t heads, dtype;
+} awq_rows;
+
+/* Cosines and sines of the rotary positions.
+ *   table  float [n_pos, rot_dim / 2, 2] (device): (cos, sin) of pos * f_i times
+ *          the magnitude, i < rot_dim / 2, formed in binary64 and rounded once
+ *   f_i = base^(-2 i / rot_dim), then by `kind`, for contexts longer than the
+ *   model was trained on:
+ *     AWQ_ROPE_PLAIN    f_i
+ *     AWQ_ROPE_LINEAR   f_i / factor
+ *     AWQ_ROPE_NTK      base * factor^(rot_dim / (rot_dim - 2)) in place of base
+ *     AWQ_ROPE_YARN     f_i (1 - w_i) + f_i / factor * w_i, w_i = clamp((i - lo) / (hi - lo), 0, 1),
+ *                       lo (hi) the pair, rounded down (up), that turns beta_fast
+ *                       (beta_slow) times over `original` positions; the magnitude
+ *                       given, or 0.1 ln(factor) + 1 if it is 0
+ *   1 <= factor <= 1e6; rot_dim even; 1 < base <= 1e12. */
+enum { AWQ_ROPE_PLAIN = 0, AWQ_ROPE_LINEAR = 1, AWQ_ROPE_NTK = 2, AWQ_ROPE_YARN = 3 };
+typedef struct {
+    int32_t kind;
+    double factor, original, beta_fast, beta_slow, magnitude;
+} awq_rope_scaling;
+AWQ_API awq_status awq_rope_table(int64_t n_pos, int32_t rot_dim, double base, awq_rope_scaling scaling,
+                                  float *table, void *stream);
+
+/* Rotary positions: pair i of the first rot_dim elements of every head turns by
+ * the angle of its row's position,
+ *   y1 = RN32(RN32(x1 c) - RN32(x2 s)),  y2 = RN32(RN32(x2 c) + RN32(x1 s)),
+ * rounded once to y's type; elements past rot_dim are copied.
+ *   layout     AWQ_ROPE_HALF: pair i is (i, i + rot_dim / 2); AWQ_ROPE_INTERLEAVED:
+ *              (2 i, 2 i + 1)
+ *   positions  int32 [T] (device).  One outside [0, n_pos) leaves its row of y as
+ *              it was and raises AWQ_ERR_INVALID_ARG through awq_get_status().
+ *   inverse    1: by minus the angle -- for a table of magnitude 1 the inverse, for
+ *              every table the transpose, so also the gradient: dx = rope(dy, inverse)
+ * x and y: any of the three types and any strides, head_dim even, rot_dim even and
+ * <= head_dim; y may be x itself (same type and strides), otherwise they may not
+ * overlap.  16-byte accesses where base and strides (multiples of 8 elements),
+ * head_dim (8) and rot_dim (8; 16 in the half layout) allow them; y's base must be
+ * aligned to its element in any case. */
+enum { AWQ_ROPE_HALF = 0, AWQ_ROPE_INTERLEAVED = 1 };
+typedef struct {
+    const float *table;
+    int64_t n_pos;
+    int32_t rot_dim, layout;
+} awq_rope_cfg;
+AWQ_API awq_status awq_rope(awq_rows x, awq_rows y, int64_t T, int32_t head_dim, const int32_t *positions,
+                            awq_rope_cfg rope, int32_t inverse, void *stream);
+
+/* A paged cache: n_pages pages of page_size tokens (16, 32, 64, 128 or 256), heads
+ * key/value heads of head_dim 64 or 128.
+ *   k_codes, v_codes    e4m3 [n_pages, heads, page_size, head_dim]
+ *   k_scales, v_scales  float [n_pages, heads, page_size / 16]: one power of two
+ *                       2^e, -40 <= e <= 40, for each block of 16 tokens and head;
+ *                       a value is code * scale
+ * n_pages * heads * page_size < 2^31.
+ *
+ * A batch of sequences with new tokens:
+ *   seq_lens   int32 [n_seqs]: tokens of each sequence in the cache, the new ones included
+ *   cu_tokens  int32 [n_seqs + 1], not decreasing, or NULL: the new tokens of sequence b
+ *              are rows cu[b] .. cu[b + 1] - 1 of k, v, q; they take its last positions.
+ *              NULL: one new token each, row b (T = n_seqs).
+ *   pages      int32 [n_seqs, page_stride], the first max_pages of a row valid:
+ *              position p of sequence b is in page pages[b, p / page_size]
+ * Rows at or past cu[n_seqs] belong to nobody and are left as they are; a row whose
+ * position would be negative (a padded row of an empty sequence) has no place in the
+ * cache and sees no keys.  A position past max_pages * page_size, and a page outside
+ * [0, n_pages), raise AWQ_ERR_INVALID_ARG through awq_get_status(); nothing is read
+ * or written there.                                                            */
+typedef struct {
+    void *k_codes, *v_codes;
+    float *k_scales, *v_scales;
+    int64_t n_pages;
+    int32_t page_size, heads, head_dim;
+} awq_kv_cache;
+typedef struct {
+    const int32_t *seq_lens, *cu_tokens, *pages;
+    int64_t n_seqs, page_stride, max_pages;
+} awq_kv_batch;
+
+/* Append the new tokens' keys and values, the keys rotated to their positions on the
+ * way, and (optionally) rotate the same tokens' queries.
+ *   k, v     rows of c.heads heads, one type
+ *   rope     as in awq_rope, of the cache's positions; table NULL: no rotation
+ *   q        rows of k's type, data NULL: none; q_out its rotated rows, any type
+ * Per block of 16 positions and head that gets tokens:
+ *   e     the least exponent in [-40, 40] with |y| <= 448 * 2^e for every finite new
+ *         value y (k rotated in binary32, or v), and not less than the exponent of
+ *         the block's earlier tokens, whose codes are rounded anew if it rises
+ *   code  e4m3(y 2^-e), to nearest even, saturated; NaN where y is not finite
+ * Codes behind the new tokens of a block are left as they are.  Rows of q_out whose
+ * position is negative or past the table are not written.
+ * Bases 16-byte aligned, strides multiples of 8 elements.  A page that two sequences
+ * share may be read by both, but only one may append to it. */
+AWQ_API awq_status awq_kv_append(awq_kv_cache cache, awq_kv_batch batch, int64_t T, awq_rows k, awq_rows v,
+                                 awq_rows q, awq_rows q_out, awq_rope_cfg rope, void *stream);
+
+/* Attention of the new tokens over the cache (their own keys appended before):
+ *   out[t, h] = sum_j softmax_j(scale q[t, h] . k[j, h']) v[j, h'],
+ * h' = h / (q.heads / c.heads), over the keys j <= p of row t's sequence, p its
+ * position, and with window > 0 only j > p - window.  A row that sees no key gives 0
+ * (lse -inf).  Scores, softmax statistics and sums are binary32; the products' operands
+ * are exact (codes) or q's values; probabilities are rounded to fp16 for the second product.
+ *   q, out      rows of q.heads heads (a multiple of c.heads), fp16 or bf16, the same type
+ *   max_tokens  the most new tokens any sequence has (1 without cu_tokens)
+ *   lse         float [T, q.heads] or NULL: ln sum_j exp(scale q . k_j)
+ *   ws          ws_bytes >= awq_kv_attention_workspace_bytes(...), 256-byte aligned;
+ *               overwritten by every call: calls that share it must be ordered
+ * Bases 16-byte aligned, strides multiples of 8 elements; out may not overlap q. */
+AWQ_API size_t awq_kv_attention_workspace_bytes(awq_kv_cache cache, int64_t T, int32_t q_heads,
+                                                int32_t max_tokens);
+AWQ_API awq_status awq_kv_attention(awq_kv_cache cache, awq_kv_batch batch, int64_t T, awq_rows q, awq_rows out,
+                                    float scale, int32_t max_tokens, int64_t window, float *lse, void *ws,
+                                    size_t ws_bytes, void *stream);
 
 /* Self-test of device-side failure detection (no counterpart on the pages: it
  * checks the library, not the method).  Launches one warp that waits on a

@@ -1,0 +1,625 @@
+"""The cache operators on the GPU against their oracle.
+
+Acceptance:
+  * rotation: bit-exact (every binary32 operation is pinned, one rounding to the
+    result's type); the table: half a unit of binary32 beside the binary64 value;
+  * append: codes and scales bit-exact, every other byte of the cache untouched;
+  * attention: the tolerance of `bound` below, derived from the roundings.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import kv as okv
+
+pytestmark = pytest.mark.gpu
+
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def awq():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import awq_activation_aware_b200 as m
+    m.set_wait_timeout_ms(2000)
+    return m
+
+
+def dev(x, dtype=None):
+    t = torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    return t if dtype is None else t.to(dtype)
+
+
+def ints(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+# ----- rotary positions ---------------------------------------------------------
+@pytest.mark.parametrize("kw", [dict(), dict(scaling="linear", factor=3.0), dict(scaling="ntk", factor=4.0),
+                                dict(scaling="yarn", factor=8.0, original=4096.0),
+                                dict(base=5e5, scaling="yarn", factor=16.0, original=8192.0, beta_fast=16.0,
+                                     beta_slow=2.0, magnitude=1.25)])
+@pytest.mark.parametrize("n,rot", [(1, 2), (131072, 64), (1000, 128), (777, 20)])
+def test_rope_table(awq, n, rot, kw):
+    if kw.get("scaling") == "ntk" and rot == 2:
+        pytest.skip("ntk has no exponent for one pair")
+    t = f64(awq.rope_table(n, rot, **kw))
+    awq.get_status()
+    ref = okv.rope_table(n, rot, **kw)
+    # one rounding to binary32 (2^-24 of the value), and binary64 angles up to n off by a few 2^-53 of themselves
+    assert np.all(np.abs(t - ref) <= 2.0 ** -24 * np.abs(ref) + 16 * (n + 1) * 2.0 ** -53)
+
+
+def _rounded(y32, dtype):
+    return torch.from_numpy(y32).to(dtype)
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("T,H,D,rot", [(1, 1, 2, 2), (5, 3, 128, 128), (33, 8, 128, 64), (7, 2, 80, 20), (64, 5, 64, 64),
+                                       (3, 2, 6, 4), (9, 40, 256, 32), (200, 1, 128, 128)])
+def test_rope(awq, T, H, D, rot, layout):
+    rng = np.random.default_rng(T * 1000 + D)
+    table = awq.rope_table(300, rot, scaling="yarn", factor=4.0, original=64.0)
+    cs = table.cpu().numpy()
+    pos = rng.integers(0, 300, T)
+    x = rng.standard_normal((T, H, D)).astype(np.float32)
+    for src in (F32, F16, BF16):
+        xd = dev(x, src)
+        for dst in (F32, F16, BF16):
+            for inverse in (False, True):
+                y = awq.rope(xd, ints(pos), table, layout, inverse, dtype=dst)
+                ref = okv.rotate(xd.float().cpu().numpy(), cs[pos], layout, inverse)
+                assert torch.equal(y.cpu(), _rounded(ref, dst)), (src, dst, inverse)
+        z = awq.rope(xd.clone(), ints(pos), table, layout)
+        w = xd.clone()
+        assert awq.rope(w, ints(pos), table, layout, out=w) is w           # in place
+        assert torch.equal(z, w)
+    awq.get_status()
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rope_strided_and_unaligned_rows(awq, layout):
+    table = awq.rope_table(50, 64)
+    pos = ints(np.arange(11))
+    base = torch.randn((11, 300, 64), device="cuda", dtype=F16)
+    big = torch.randn(11 * 3 * 64 + 1, device="cuda", dtype=F16)
+    views = {"slice of a projection": base[:, 10:14], "every other head": base[:, ::100],
+             "heads first": torch.randn((3, 11, 64), device="cuda", dtype=F16).transpose(0, 1),
+             "one element off": big[1:].view(11, 3, 64), "one row for all": base[:1, :4].expand(11, 4, 64)}
+    for name, x in views.items():
+        ref = okv.rotate(x.float().cpu().numpy(), table.cpu().numpy()[:11], layout)
+        assert torch.equal(awq.rope(x, pos, table, layout).cpu(), _rounded(ref, F16)), name
+        out = torch.full((11, x.shape[1] + 2, 65), 7.0, device="cuda", dtype=F16)
+        awq.rope(x, pos, table, layout, out=out[:, 1:-1, :64])
+        assert torch.equal(out[:, 1:-1, :64].cpu(), _rounded(ref, F16)), name
+        assert bool((out[:, 0] == 7).all() and (out[:, -1] == 7).all() and (out[..., 64] == 7).all()), name
+    with pytest.raises(awq.AWQError):                                      # written rows would overlap
+        awq.rope(base[:, :4], pos, table, out=base[:1, :4].expand(11, 4, 64))
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+def test_rope_inverse_is_the_gradient(awq, layout):
+    rng = np.random.default_rng(5)
+    table = awq.rope_table(40, 32, scaling="yarn", factor=4.0, original=10.0)      # magnitude above 1
+    x, w = rng.standard_normal((4, 2, 48)).astype(np.float32), rng.standard_normal((4, 2, 48)).astype(np.float32)
+    pos = ints([3, 39, 0, 17])
+    g = f64(awq.rope(dev(w), pos, table, layout, inverse=True))
+    # against the formula: the transpose of the rotation, with the table's own entries in binary64
+    ref = okv.rotate(w.astype(np.float64), table.cpu().numpy().astype(np.float64)[[3, 39, 0, 17]], layout, True)
+    np.testing.assert_allclose(g, ref, atol=3 * 2.0 ** -24 * np.abs(w).max() * 1.2, rtol=0)
+    # against differences: the map is linear, so a step of 1 is exact but for the roundings of the two results,
+    # each of three operations (3 * 2^-24) on values up to 1.14 (|x1| + |x2|) <= 12
+    for i in range(0, x.size, 7):
+        e = np.zeros(x.size, np.float32)
+        e[i] = 1.0
+        hi = f64(awq.rope(dev(x + e.reshape(x.shape)), pos, table, layout))
+        lo = f64(awq.rope(dev(x - e.reshape(x.shape)), pos, table, layout))
+        d = ((hi - lo) / 2 * w).sum()
+        assert abs(d - g.reshape(-1)[i]) <= 2 * 2 * 4 * 2.0 ** -24 * 12 * np.abs(w).max()
+
+
+def test_rope_position_outside_the_table_is_reported(awq):
+    table = awq.rope_table(8, 64)
+    x = torch.randn((3, 2, 64), device="cuda", dtype=F16)
+    out = torch.full_like(x, 5.0)
+    awq.rope(x, ints([7, 8, -1]), table, out=out)
+    with pytest.raises(awq.AWQError):
+        awq.get_status()
+    assert bool((out[1:] == 5).all()) and not bool((out[0] == 5).all())
+    awq.rope(x, ints([0, 1, 2]), table)
+    awq.get_status()
+
+
+# ----- append -------------------------------------------------------------------
+def _random_cache(rng, n_pages, H, P, D):
+    """Codes of every value that is not NaN, scales powers of two."""
+    c = {}
+    for w in "kv":
+        codes = rng.integers(0, 256, (n_pages, H, P, D)).astype(np.uint8)
+        codes[(codes & 127) == 127] = 3
+        c[w + "_codes"] = codes
+        c[w + "_scales"] = (2.0 ** rng.integers(-12, -6, (n_pages, H, P // 16))).astype(np.float32)
+    return c
+
+
+def _upload(c):
+    return {k: dev(x).view(torch.float8_e4m3fn) if k.endswith("codes") else dev(x) for k, x in c.items()}
+
+
+def _same(cache, ref):
+    for k, x in ref.items():
+        got = cache[k].view(torch.uint8).cpu().numpy() if k.endswith("codes") else cache[k].cpu().numpy()
+        np.testing.assert_array_equal(got, x, err_msg=k)
+
+
+def _pages(rng, lens, P, extra=0):
+    """A page table of distinct pages in random order (unused entries point far outside), and the pool's size."""
+    need = [-(-int(n) // P) for n in lens]
+    order = rng.permutation(sum(need) + extra).astype(np.int32)
+    t = np.full((len(lens), max(max(need), 1) + 1), 1 << 30, np.int32)
+    at = 0
+    for b, n in enumerate(need):
+        t[b, :n] = order[at:at + n]
+        at += n
+    return t, max(len(order), 1)
+
+
+APPENDS = [  # lengths after the append, new tokens of each (None: one each)
+    ([1], None), ([16], None), ([17], None), ([33, 1, 0, 64, 65, 7], None), ([5, 40, 16, 100], [5, 24, 16, 1]),
+    ([300, 0, 3, 129], [77, 0, 3, 129]), ([31, 48], [15, 17]), ([2], [3]),
+]
+
+
+@pytest.mark.parametrize("lens,new", APPENDS)
+@pytest.mark.parametrize("P,H,D,layout,rot", [(16, 2, 64, "half", 64), (64, 3, 128, "interleaved", 128),
+                                              (32, 1, 128, "half", 20), (256, 2, 64, "interleaved", 6),
+                                              (128, 2, 128, None, 0)])
+def test_append(awq, lens, new, P, H, D, layout, rot):
+    rng = np.random.default_rng(len(lens) * 100 + P)
+    cu = None if new is None else np.concatenate([[0], np.cumsum(new)])
+    T = len(lens) if new is None else int(cu[-1]) + 3                      # three rows that belong to nobody
+    pages, n_pages = _pages(rng, lens, P, 2)
+    base = _random_cache(rng, n_pages, H, P, D)
+    table = awq.rope_table(max(max(lens), 1), rot) if rot else None
+    HQ = 5
+    x = (rng.standard_normal((T, HQ + 2 * H, D)) * 4.0 ** rng.integers(-3, 3, (T, 1, 1))).astype(np.float32)
+    for src in (F32, F16, BF16):
+        xd = dev(x, src)
+        xf = xd.float().cpu().numpy()
+        cache, ref = _upload(base), {k: v.copy() for k, v in base.items()}
+        q, k, v = xd[:, :HQ], xd[:, HQ:HQ + H], xd[:, HQ + H:]
+        q_out = torch.full((T, HQ, D), 9.0, device="cuda", dtype=BF16)
+        got = awq.kv_append(cache, k, v, ints(lens), ints(pages), None if cu is None else ints(cu), table,
+                            layout or "half", q=q if rot else None, q_out=q_out if rot else None)
+        awq.get_status()
+        cs = table.cpu().numpy() if rot else None
+        okv.append(ref, xf[:, HQ:HQ + H], xf[:, HQ + H:], lens, pages, cu, cs, layout or "half")
+        _same(cache, ref)
+        if not rot:
+            assert got is None
+            continue
+        assert got is q_out
+        places = okv.rows_of(lens, cu, T)
+        for t, p in enumerate(places):
+            if p is None or p[1] < 0:
+                assert bool((q_out[t] == 9).all())
+            else:
+                y = okv.rotate(xf[t:t + 1, :HQ], cs[[p[1]]], layout)
+                assert torch.equal(q_out[t:t + 1].cpu(), _rounded(y, BF16))
+
+
+def test_append_token_by_token(awq):
+    """Every growth of every block on the way, each step bit-exact."""
+    rng = np.random.default_rng(8)
+    H, D, P = 2, 128, 32
+    pages = np.array([[2, 0, 1], [3, 5, 4]], np.int32)
+    ref = _random_cache(rng, 6, H, P, D)
+    cache = _upload(ref)
+    table = awq.rope_table(96, D)
+    for n in range(1, 70):
+        k, v = ((rng.standard_normal((2, H, D)) * 2.0 ** rng.integers(-8, 9, (2, H, 1))).astype(np.float32) for _ in "kv")
+        awq.kv_append(cache, dev(k), dev(v), ints([n, n + 9]), ints(pages), table=table)
+        okv.append(ref, k, v, [n, n + 9], pages, None, table.cpu().numpy())
+    awq.get_status()
+    _same(cache, ref)
+
+
+def test_append_values_at_the_edges(awq):
+    """Zeros, infinities and NaN (stored as NaN, out of the scale), values past both ends of the scales, ties."""
+    D, P = 64, 16
+    x = np.zeros((6, 1, D), np.float32)
+    x[1, 0, :8] = [np.inf, -np.inf, np.nan, 1.0, -448.0, 448.0, 0.5, -0.0]
+    x[2, 0, :4] = [3e38, -1e30, 1.0, 0.0]
+    x[3, 0, :4] = [1e-38, 2e-45, -1e-20, 0.0]
+    x[4, 0] = np.arange(D) / 64 + 1                                       # ties of the three fraction bits
+    x[5, 0] = np.nan
+    ref = _random_cache(np.random.default_rng(0), 6, 1, P, D)
+    cache, pages = _upload(ref), np.arange(6, dtype=np.int32)[:, None]
+    awq.kv_append(cache, dev(x), dev(x), ints([1] * 6), ints(pages))
+    okv.append(ref, x, x, [1] * 6, pages)
+    _same(cache, ref)
+    # the same in the middle of a block
+    awq.kv_append(cache, dev(x[::-1].copy()), dev(x), ints([2] * 6), ints(pages))
+    okv.append(ref, x[::-1], x, [2] * 6, pages)
+    awq.get_status()
+    _same(cache, ref)
+
+
+def test_append_reports_pages_and_positions_outside(awq):
+    rng = np.random.default_rng(1)
+    ref = _random_cache(rng, 4, 1, 16, 64)
+    cache = _upload(ref)
+    x = rng.standard_normal((4, 1, 64)).astype(np.float32)
+    pages = np.array([[0, 1], [4, 1], [-1, 2], [3, 2]], np.int32)
+    lens = [17, 5, 3, 40]                                                  # fine, two bad pages, past the table's 32
+    awq.kv_append(cache, dev(x), dev(x), ints(lens), ints(pages))
+    with pytest.raises(awq.AWQError):
+        awq.get_status()
+    okv.append(ref, x[:1], x[:1], lens[:1], pages[:1])
+    _same(cache, ref)
+    awq.kv_append(cache, dev(x[:1]), dev(x[:1]), ints([18]), ints(pages[:1]), table=awq.rope_table(17, 64))
+    with pytest.raises(awq.AWQError):                                      # past the rotary table
+        awq.get_status()
+    _same(cache, ref)
+
+
+# ----- attention ----------------------------------------------------------------
+def bound(out, info, dtype, D):
+    """What the roundings can add up to.  Probabilities are rounded to fp16 (2^-11 of each, or 2^-22 of the largest
+    where fp16 is subnormal), scores are binary32 sums of D exact products (each addition at most 2^-23 of the sum of
+    the magnitudes, twice a rounding to nearest since the tensor cores may truncate) and the exponential is off by
+    2^-22: all relative to the mass sum p |v|; sums over n keys add n / 8 such additions; the result is rounded once."""
+    mass, reach, peak, keys = info
+    delta = (D + 8) * 2.0 ** -23 * reach
+    rel = 2.0 ** -11 + 2 * delta + 2.0 ** -21 + (keys / 8 + 64) * 2.0 ** -23
+    eps = torch.finfo(dtype).eps / 2
+    tiny = 2.0 ** -25 if dtype == F16 else 0.0                             # half a step of subnormal fp16
+    return (1 + eps) * (mass * rel[..., None] * 2 + (keys * 2.0 ** -22 * peak)[..., None]) + eps * np.abs(out) + tiny
+
+
+def lse_bound(lse, info, D):
+    _, reach, _, keys = info
+    return (D + 8) * 2.0 ** -23 * reach + (keys / 8 + 64) * 2.0 ** -23 + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0))
+
+
+def _attend_case(seed, lens, new, H, G, D, P, spoil=True):
+    rng = np.random.default_rng(seed)
+    cu = None if new is None else np.concatenate([[0], np.cumsum(new)])
+    T = len(lens) if new is None else int(cu[-1])
+    pages, n_pages = _pages(rng, lens, P, 1)
+    c = {}
+    for w in "kv":
+        x = rng.standard_normal((n_pages, H, P // 16, 16, D))
+        if w == "k":
+            x *= np.exp(0.7 * rng.standard_normal(D))
+        e = np.ceil(np.log2(np.abs(x).max((3, 4)) / 448))
+        codes = okv.e4m3_encode(x * 2.0 ** -e[..., None, None]).reshape(n_pages, H, P, D)
+        e += rng.integers(-3, 4, e.shape)                                  # blocks of very different sizes
+        c[w + "_codes"], c[w + "_scales"] = codes, (2.0 ** e).astype(np.float32)
+    if spoil:                                                              # NaN wherever no token is
+        seen = np.zeros((n_pages, P), bool)
+        for b, n in enumerate(lens):
+            for j in range(n):
+                seen[pages[b, j // P], j % P] = True
+        for w in "kv":
+            c[w + "_codes"].transpose(0, 2, 1, 3)[~seen] = 127
+            blocks = ~seen.reshape(n_pages, P // 16, 16).any(-1)
+            c[w + "_scales"].transpose(0, 2, 1)[blocks] = np.nan
+    q = rng.standard_normal((T, H * G, D))
+    return c, q, np.asarray(lens, np.int32), cu, pages
+
+
+def _attend(awq, c, q, lens, cu, pages, dtype, D, window=0, scale=None, **kw):
+    new = 1 if cu is None else max(int(np.diff(cu).max()), 1)
+    qd = dev(q, dtype)
+    out, lse = awq.kv_attention(_upload(c), qd, ints(lens), ints(pages), None if cu is None else ints(cu), new, scale,
+                                window, return_lse=True, **kw)
+    awq.get_status()
+    ref, rl, info = okv.attention(c, f64(qd), lens, pages, cu, scale, window)
+    return out, lse, ref, rl, info
+
+
+def _close(out, lse, ref, rl, info, dtype, D):
+    d = np.abs(f64(out) - ref)
+    lim = bound(ref, info, dtype, D)
+    assert np.all(d <= lim), (float((d / lim).max()), np.unravel_index((d / lim).argmax(), d.shape))
+    empty = np.isneginf(rl)
+    got = f64(lse)
+    assert np.array_equal(np.isneginf(got), empty) and not f64(out)[empty].any()
+    assert np.all(np.abs(got[~empty] - rl[~empty]) <= lse_bound(rl, info, D)[~empty])
+
+
+SINGLES = [[1], [16], [17], [0, 15, 64, 65], [63, 0, 128, 129, 1], [1000], [517, 2049, 33]]
+HEADS = [(1, 1), (2, 4), (1, 8), (3, 5), (2, 16), (1, 32), (8, 1)]
+
+
+@pytest.mark.parametrize("lens", SINGLES)
+@pytest.mark.parametrize("H,G", HEADS)
+def test_attention_single_tokens(awq, lens, H, G):
+    i = SINGLES.index(lens) + HEADS.index((H, G))
+    P, D, dtype = [16, 64, 32, 128, 256][i % 5], [64, 128][i % 2], [F16, BF16][(i // 2) % 2]
+    c, q, lens, cu, pages = _attend_case(i, lens, None, H, G, D, P)
+    _close(*_attend(awq, c, q, lens, cu, pages, dtype, D), dtype, D)
+
+
+@pytest.mark.parametrize("P", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_attention_every_page_size(awq, P, D, dtype):
+    c, q, lens, cu, pages = _attend_case(P + D, [300, 1, 77], None, 2, 4, D, P)
+    _close(*_attend(awq, c, q, lens, cu, pages, dtype, D), dtype, D)
+
+
+RAGGED = [  # lengths, new tokens
+    ([5], [5]), ([64], [3]), ([300, 40, 0, 129], [7, 40, 0, 1]), ([1000], [130]), ([257, 600], [257, 2]),
+    ([33, 500, 1, 90], [33, 129, 1, 64]), ([2, 10], [5, 4]), ([1537], [513]),
+]
+
+
+@pytest.mark.parametrize("lens,new", RAGGED)
+@pytest.mark.parametrize("H,G", [(1, 1), (2, 4), (1, 8), (2, 5), (1, 7)])
+def test_attention_several_tokens(awq, lens, new, H, G):
+    i = RAGGED.index((lens, new)) * 3 + H + G
+    P, D, dtype = [16, 64, 32, 128, 256][i % 5], [128, 64][i % 2], [BF16, F16][(i // 2) % 2]
+    c, q, lens, cu, pages = _attend_case(i, lens, new, H, G, D, P)
+    _close(*_attend(awq, c, q, lens, cu, pages, dtype, D), dtype, D)
+
+
+@pytest.mark.parametrize("window", [1, 5, 16, 64, 100, 5000])
+@pytest.mark.parametrize("new", [None, [1, 40, 3, 200]])
+def test_attention_window(awq, window, new):
+    c, q, lens, cu, pages = _attend_case(window, [1, 300, 64, 701], new, 2, 4, 64 if new else 128, 32)
+    D = q.shape[2]
+    _close(*_attend(awq, c, q, lens, cu, pages, F16, D, window=window), F16, D)
+
+
+@pytest.mark.parametrize("scale", [1e-3, 1.0, 4.0])
+@pytest.mark.parametrize("new", [None, [90]])
+def test_attention_flat_and_sharp_rows(awq, scale, new):
+    """Scores from nearly equal to one key taking everything."""
+    c, q, lens, cu, pages = _attend_case(int(scale * 100), [700], new, 2, 4, 128, 64)
+    _close(*_attend(awq, c, q, lens, cu, pages, F16, 128, scale=scale), F16, 128)
+
+
+@pytest.mark.parametrize("new", [None, [70]])
+def test_attention_dominant_key_with_small_value(awq, new):
+    """One key takes nearly all the weight and its value block is tiny: the others' values decide the result."""
+    c, q, lens, cu, pages = _attend_case(3, [400], new, 1, 4, 128, 64)
+    page = pages[0, 0]
+    c["k_codes"][page, :, 0] = okv.e4m3_encode(np.full(128, 200.0))
+    q = np.abs(q)
+    c["v_scales"][page, :, 0] = 2.0 ** -30
+    _close(*_attend(awq, c, q, lens, cu, pages, F16, 128), F16, 128)
+
+
+def test_attention_of_zero_values(awq):
+    """Blocks of zeros have the least scale; they still take their weight."""
+    c, q, lens, cu, pages = _attend_case(4, [100], None, 1, 8, 64, 32)
+    c["v_codes"][pages[0, 0]] = 0
+    c["v_scales"][pages[0, 0]] = 2.0 ** -40
+    _close(*_attend(awq, c, q, lens, cu, pages, BF16, 64), BF16, 64)
+
+
+@pytest.mark.parametrize("new", [None, [1, 40]])
+def test_attention_extreme_scales(awq, new):
+    """Value blocks from the least to the largest scale; keys whose scores stay finite."""
+    c, q, lens, cu, pages = _attend_case(5, [90, 200], new, 2, 2, 64, 16)
+    ids = pages[pages < (1 << 30)]
+    c["v_scales"][ids[::2]] = 2.0 ** -40
+    c["v_scales"][ids[1::2]] = 2.0 ** 6
+    _close(*_attend(awq, c, q, lens, cu, pages, BF16, 64), BF16, 64)
+
+
+@pytest.mark.parametrize("new", [None, [3, 2], [50, 40]])
+def test_attention_strided_rows_and_rows_of_nobody(awq, new):
+    c, q, lens, cu, pages = _attend_case(6, [70, 81], new, 2, 4, 128, 64)
+    T = q.shape[0]
+    ref, rl, info = okv.attention(c, f64(dev(q, F16)), lens, pages, cu)
+    pad = 0 if new is None else 2
+    big = torch.full((T + pad, 20, 128), float("nan"), device="cuda", dtype=F16)
+    big[:T, 3:11] = dev(q, F16)
+    out = torch.full((T + pad, 10, 136), 7.0, device="cuda", dtype=F16)
+    qd, od = big[:, 3:11], out[:, 1:9, :128]
+    kw = dict(cu_tokens=None if cu is None else ints(cu), max_tokens=1 if new is None else max(new))
+    wide = torch.full((2, pages.shape[1] + 3), 1 << 30, dtype=torch.int32, device="cuda")
+    wide[:, :pages.shape[1]] = ints(pages)
+    got, lse = awq.kv_attention(_upload(c), qd, ints(lens), wide[:, :pages.shape[1]], out=od, return_lse=True, **kw)
+    awq.get_status()
+    assert got is od
+    _close(od[:T], lse[:T], ref, rl, info, F16, 128)
+    rest = out.clone()
+    rest[:T, 1:9, :128] = 7.0
+    assert bool((rest == 7).all())
+
+
+@pytest.mark.parametrize("new", [None, [40, 9]])
+def test_attention_reports_pages_outside(awq, new):
+    """A bad page is reported and read as if its keys were not there; the other sequence is as ever."""
+    c, q, lens, cu, pages = _attend_case(7, [100, 90], new, 2, 4, 64, 32)
+    good = _attend(awq, c, q, lens, cu, pages, F16, 64)
+    bad = pages.copy()
+    bad[0, 1], bad[0, 2] = c["k_codes"].shape[0], -5
+    n = 1 if new is None else max(new)
+    out = awq.kv_attention(_upload(c), dev(q, F16), ints(lens), ints(bad), None if cu is None else ints(cu), n)
+    with pytest.raises(awq.AWQError):
+        awq.get_status()
+    first = 1 if new is None else new[0]
+    assert torch.equal(out[first:], good[0][first:])
+    assert bool(torch.isfinite(out).all())
+    long = awq.kv_attention(_upload(c), dev(q, F16), ints([100, 10 ** 6]), ints(pages),
+                            None if cu is None else ints(cu), n)
+    with pytest.raises(awq.AWQError):                                      # longer than the table
+        awq.get_status()
+    assert torch.equal(long[:first], good[0][:first])
+
+
+def test_attention_far_pages(awq):
+    """Pages whose codes lie past 4 GiB."""
+    H, P, D, n_pages = 8, 64, 128, 70000
+    cache = awq.kv_cache(n_pages, H, P, D)
+    assert cache["k_codes"].numel() > 1 << 32
+    c, q, lens, cu, pages = _attend_case(9, [200], None, H, 2, D, P, spoil=False)
+    far = np.array([[n_pages - 1, 3, n_pages - 2, 68000, 0]], np.int32)[:, :pages.shape[1]]
+    for k in c:
+        for i, j in zip(far[0], pages[0]):
+            if j < len(c[k]):
+                cache[k].view(torch.uint8 if "codes" in k else F32)[int(i)] = dev(c[k][j])
+    qd = dev(q, F16)
+    ref, rl, info = okv.attention(c, f64(qd), lens, pages)
+    out, lse = awq.kv_attention(cache, qd, ints(lens), ints(far), return_lse=True)
+    awq.get_status()
+    _close(out, lse, ref, rl, info, F16, D)
+    out, lse = awq.kv_attention(cache, qd, ints(lens), ints(far), cu_tokens=ints([0, 1]), max_tokens=100, return_lse=True)
+    _close(out, lse, ref, rl, info, F16, D)
+    # and appended there
+    x = torch.randn((1, H, D), device="cuda", dtype=F16)
+    before = {k: cache[k].view(torch.uint8 if "codes" in k else F32)[n_pages - 2].clone() for k in cache}
+    ref = {k: v.cpu().numpy()[None] for k, v in before.items()}
+    awq.kv_append(cache, x, x, ints([150]), ints(far))
+    awq.get_status()
+    okv.append(ref, x.float().cpu().numpy(), x.float().cpu().numpy(), [150 - 128], np.array([[0]]))
+    _same({k: cache[k][n_pages - 2:n_pages - 1] for k in cache}, ref)
+
+
+@pytest.mark.parametrize("new", [None, [4, 2, 3], [90, 120, 10]])
+def test_attention_repeats_to_the_bit(awq, new):
+    c, q, lens, cu, pages = _attend_case(10, [3000, 500, 1111], new, 2, 8, 128, 64)
+    a = _attend(awq, c, q, lens, cu, pages, BF16, 128)
+    b = _attend(awq, c, q, lens, cu, pages, BF16, 128)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    _close(*a, BF16, 128)
+
+
+@pytest.mark.parametrize("new", [None, [5, 3], [60, 130]])
+def test_captured_steps_share_a_workspace(awq, new):
+    """Two captured graphs with one workspace, replayed in turn with other lengths, on a stream of their own."""
+    cases = [_attend_case(20 + i, [900, 333], new, 2, 4, 128, 64) for i in range(2)]
+    n = 1 if new is None else max(new)
+    ws = torch.empty(awq.kv_attention_workspace_bytes(_upload(cases[0][0]), cases[0][1].shape[0], 8, n),
+                     dtype=torch.uint8, device="cuda")
+    ws.fill_(0xff)
+    side, graphs = torch.cuda.Stream(), []
+    for c, q, lens, cu, pages in cases:
+        s = dict(cache=_upload(c), q=dev(q, F16), lens=ints(lens), pages=ints(pages), cu=None if cu is None else ints(cu))
+        s["out"] = torch.zeros(q.shape, device="cuda", dtype=F16)
+        call = lambda s=s: awq.kv_attention(s["cache"], s["q"], s["lens"], s["pages"], s["cu"], n, out=s["out"],  # noqa: E731
+                                            workspace=ws)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            call()
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=side):
+                call()
+        s["out"].zero_()
+        graphs.append((g, s))
+    torch.cuda.synchronize()
+    for lens in ([900, 333], [700, 332]):
+        for (g, s), (c, q, _, cu, pages) in zip(graphs, cases):
+            s["lens"].copy_(ints(lens))
+            g.replay()
+        torch.cuda.synchronize()
+        for (g, s), (c, q, _, cu, pages) in zip(graphs, cases):
+            ref, _, info = okv.attention(c, f64(s["q"]), lens, pages, cu)
+            assert np.all(np.abs(f64(s["out"]) - ref) <= bound(ref, info, F16, 128))
+    awq.get_status()
+
+
+def test_another_stream_than_the_current_one(awq):
+    c, q, lens, cu, pages = _attend_case(30, [640], None, 2, 4, 128, 64)
+    side = torch.cuda.Stream()
+    s = [_upload(c), dev(q, F16), ints(lens), ints(pages)]
+    x = torch.randn((1, 2, 128), device="cuda")
+    table = awq.rope_table(700, 128)
+    torch.cuda.synchronize()
+    y = awq.rope(x, ints([5]), table, stream=side)
+    out, lse = awq.kv_attention(*s, return_lse=True, stream=side)
+    awq.kv_append(s[0], x, x, s[2], s[3], table=table, stream=side)
+    side.synchronize()
+    awq.get_status(side)
+    assert torch.equal(y, awq.rope(x, ints([5]), table))
+    ref, rl, info = okv.attention(c, f64(s[1]), lens, pages)
+    _close(out, lse, ref, rl, info, F16, 128)
+
+
+def test_binding_refuses(awq):
+    cache = awq.kv_cache(4, 2, 16, 64)
+    x = torch.zeros((2, 2, 64), device="cuda", dtype=F16)
+    lens, pages = ints([1, 1]), ints([[0], [1]])
+    with pytest.raises(ValueError):
+        awq.kv_append(cache, x, x, lens, pages, q=x)                       # q without a table
+    with pytest.raises(ValueError):
+        awq.kv_append(cache, x[:1], x[:1], lens, pages)                    # one row, two sequences
+    with pytest.raises(ValueError):
+        awq.kv_attention(cache, torch.zeros((2, 2, 128), device="cuda", dtype=F16), lens, pages)
+    with pytest.raises(TypeError):
+        awq.kv_attention(cache, x, lens.long(), pages)
+    with pytest.raises(TypeError):
+        awq.kv_attention({**cache, "k_codes": cache["k_codes"].half()}, x, lens, pages)
+    with pytest.raises(ValueError):
+        awq.kv_attention({**cache, "v_scales": cache["v_scales"][:2]}, x, lens, pages)
+    with pytest.raises(ValueError):
+        awq.kv_attention(cache, x.transpose(1, 2), lens, pages)
+    with pytest.raises(awq.AWQError):
+        awq.kv_attention(cache, x.float(), lens, pages)
+    with pytest.raises(awq.AWQError):
+        awq.kv_attention(cache, x, lens, pages, workspace=torch.empty(1, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(awq.AWQError):
+        awq.kv_attention(cache, torch.zeros((2, 3, 64), device="cuda", dtype=F16), lens, pages)
+    empty = awq.kv_attention(cache, x[:0], lens[:0], pages[:0])
+    assert empty.shape == (0, 2, 64) and awq.rope(x[:0], lens[:0], awq.rope_table(4, 64)).shape == (0, 2, 64)
+    assert awq.kv_append(cache, x[:0], x[:0], lens[:0], pages[:0]) is None
+    awq.get_status()
+
+
+# ----- a run of them together ----------------------------------------------------
+@pytest.mark.parametrize("new", [None, [40, 3]])
+def test_attention_step_of_a_quantized_block(awq, new):
+    """qkv projection, append, attention, output projection as a model's step runs them: the step equals its parts,
+    and the parts equal the oracle, over a prompt and the token after it."""
+    import oracle
+    from awq_activation_aware_b200 import synth
+    HQ, H, D, hidden, P = 8, 2, 64, 512, 32
+    W, X, _ = synth.generate(synth.make_config((HQ + 2 * H) * D, hidden, 256, bits=4, group=128, seed=3))
+    qkv = awq.quantize_layer(dev(W), dev(X))
+    Wo, Xo, _ = synth.generate(synth.make_config(hidden, HQ * D, 256, bits=4, group=128, seed=4))
+    o = awq.quantize_layer(dev(Wo), dev(Xo))
+    lens = [40, 3]
+    pages = np.array([[1, 4, 0], [2, 3, 5]], np.int32)
+    table = awq.rope_table(96, D)
+    cache = awq.kv_cache(6, H, P, D)
+    ref = {k: np.zeros(t.shape, np.uint8 if k.endswith("codes") else np.float32) for k, t in cache.items()}
+    steps = [(lens, [0, 40, 43], 40), ([41, 4], None, 1)]
+    if new is None:
+        steps = [([1, 1], None, 1), ([2, 2], None, 1)]
+    at = 0
+    for ln, cu, n in steps:
+        T = 2 if cu is None else cu[-1]
+        x = dev(X[at:at + T])
+        at += T
+        y = awq.attention_step(x, qkv, o, cache, ints(ln), ints(pages), table, HQ, None if cu is None else ints(cu), n)
+        awq.get_status()
+        # the parts, on the host
+        Y = awq.qlinear(qkv["codes"], qkv["scales"], qkv["zeros"], qkv["s_best"], x).view(T, HQ + 2 * H, D).cpu().numpy()
+        okv.append(ref, Y[:, HQ:HQ + H], Y[:, HQ + H:], ln, pages, cu, table.cpu().numpy())
+        written = {k: cache[k].view(torch.uint8 if k.endswith("codes") else F32).cpu().numpy() for k in cache}
+        pos = np.array([p[1] for p in okv.rows_of(ln, cu, T)])
+        for b, L in enumerate(ln):
+            for j in range(L):
+                for w in "kv":
+                    np.testing.assert_array_equal(written[w + "_codes"][pages[b, j // P], :, j % P],
+                                                  ref[w + "_codes"][pages[b, j // P], :, j % P])
+        q = _rounded(okv.rotate(Y[:, :HQ], table.cpu().numpy()[pos], "half"), F16)
+        a, _, info = okv.attention(ref, q.double().numpy(), ln, pages, cu)
+        a_got = awq.kv_attention(cache, q.cuda(), ints(ln), ints(pages), None if cu is None else ints(cu), n)
+        assert np.all(np.abs(f64(a_got) - a) <= bound(a, info, F16, D))
+        out = awq.qlinear(o["codes"], o["scales"], o["zeros"], o["s_best"], a_got.view(T, HQ * D))
+        assert torch.equal(y, out)
+        Yr = oracle.qlinear(o["codes"].cpu().numpy().view(np.uint32), o["scales"].cpu().numpy(), o["zeros"].cpu().numpy(),
+                            o["s_best"].cpu().numpy(), a_got.view(T, -1).cpu().numpy(), 4, 128)
+        assert np.abs(f64(y) - Yr).max() <= 1e-4 * np.abs(Yr).max()
+    awq.get_status()
