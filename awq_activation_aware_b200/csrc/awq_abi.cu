@@ -14,6 +14,7 @@
 #include "awq.h"
 #include "awq_kernels.cuh"
 #include "awq_kv.cuh"
+#include "awq_kv_decode.cuh"
 
 namespace {
 

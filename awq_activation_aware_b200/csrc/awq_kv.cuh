@@ -479,85 +479,5 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
     }
 }
 
-// ---------------------------------------------------------------------------
-// Attention, the plain form of the kernel: one block of threads per (row, query
-// head), a warp per key, running maximum and sum in binary32.
-// ---------------------------------------------------------------------------
-struct AttnArgs {
-    Cache C;
-    Batch B;
-    int64_t T;
-    Rows q, out;
-    float scale_log2;          // softmax scale * log2(e)
-    int64_t window;            // keys a query sees, its own included; 0: all
-    float *lse;                // [T][heads] or NULL
-};
-template <typename TQ, int D>
-__global__ void __launch_bounds__(128) attn_plain_kernel(const AttnArgs A) {
-    constexpr int N = D / 32;
-    __shared__ float sm[4], sl[4], so[4][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, d0 = lane * N;
-    const int64_t t = blockIdx.x;
-    const int hq = blockIdx.y, h = hq / (A.q.heads / A.C.heads);
-    const int b = seq_of_row(A.B, t);
-    if (b < 0) return;
-    const Seq s = seq_info(A.B, b, A.T);
-    const int64_t pos = s.start + (t - s.row0);
-    int64_t hi = pos + 1, lo = A.window ? hi - A.window : 0;
-    if (lo < 0) lo = 0;
-    const int64_t cap = A.B.max_pages * A.C.page;
-    if (hi > cap) {
-        hi = cap;
-        if (threadIdx.x == 0) atomicOr(&g_dev_error, kDevErrBadIndex);
-    }
-    float q[N], o[N] = {};
-    load_n(static_cast<const TQ *>(A.q.data) + t * A.q.ld_tok + hq * A.q.ld_head + d0, q);
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t j = lo + warp; j < hi; j += 4) {
-        const int64_t page = page_of(A.B, A.C, b, j);
-        if (page < 0) continue;
-        const int64_t row = (page * A.C.heads + h) * A.C.page + j % A.C.page;
-        float x = 0.0f, kv[N];
-#pragma unroll
-        for (int i = 0; i < N; i += 2) {
-            const float2 k = from_e4m3x2(*reinterpret_cast<const uint16_t *>(A.C.codes[0] + row * D + d0 + i));
-            x = fmaf(q[i], k.x, fmaf(q[i + 1], k.y, x));
-            const float2 v = from_e4m3x2(*reinterpret_cast<const uint16_t *>(A.C.codes[1] + row * D + d0 + i));
-            kv[i] = v.x;
-            kv[i + 1] = v.y;
-        }
-#pragma unroll
-        for (int i = 16; i; i >>= 1) x += __shfl_xor_sync(0xffffffffu, x, i);
-        x *= A.scale_log2 * A.C.scales[0][row / kBlock];
-        const float mn = fmaxf(m, x), f = exp2f(m - mn), p = exp2f(x - mn);
-        m = mn;
-        l = l * f + p;
-        const float w = p * A.C.scales[1][row / kBlock];
-#pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = fmaf(w, kv[i], o[i] * f);
-    }
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) so[warp][d0 + i] = o[i];
-    __syncthreads();
-    if (warp == 0) {
-        const float mx = fmaxf(fmaxf(sm[0], sm[1]), fmaxf(sm[2], sm[3]));
-        float L = 0.0f, r[N] = {};
-        for (int w = 0; w < 4; ++w) {
-            const float f = sm[w] == -INFINITY ? 0.0f : exp2f(sm[w] - mx);
-            L += f * sl[w];
-#pragma unroll
-            for (int i = 0; i < N; ++i) r[i] += f * so[w][d0 + i];
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) r[i] = L > 0.0f ? r[i] / L : 0.0f;
-        store_n(static_cast<TQ *>(const_cast<void *>(A.out.data)) + t * A.out.ld_tok + hq * A.out.ld_head + d0, r);
-        if (A.lse && lane == 0) A.lse[t * A.q.heads + hq] = L > 0.0f ? (mx + log2f(L)) * 0.6931471805599453f : -INFINITY;
-    }
-}
-
 }  // namespace kv
 }  // namespace awq

@@ -93,6 +93,56 @@ void launch_append(const awq::kv::AppendArgs &A, dim3 grid, cudaStream_t st) {
     else launch_append_dim<TI, __nv_bfloat16>(A, grid, st);
 }
 
+// Codes as a 2-D tensor of bytes [n_pages * heads * page][D], boxes of `box_rows`
+// rows swizzled over their width.
+bool encode_kv_map(CUtensorMap *m, const void *codes, const awq_kv_cache &c, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)(c.n_pages * c.heads * c.page_size)};
+    cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};
+    cuuint32_t box[2] = {(cuuint32_t)c.head_dim, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Blocks of the decode attention: two an SM.
+constexpr int64_t kDecMaxGrid = 512;
+struct DecWs {
+    size_t ml_off, o_off, total;
+};
+DecWs dec_ws(int D) {
+    DecWs w;
+    w.ml_off = round_up(kDecMaxGrid * sizeof(awq::kv::dec::Meta), 256);
+    w.o_off = w.ml_off + round_up(kDecMaxGrid * 2 * awq::kv::dec::ROWS * 2 * 4, 256);
+    w.total = w.o_off + round_up((size_t)kDecMaxGrid * 2 * awq::kv::dec::ROWS * D * 4, 256);
+    return w;
+}
+
+template <typename TQ, int D>
+cudaError_t launch_decode(awq::kv::dec::Args &A, const CUtensorMap &mk, const CUtensorMap &mv, unsigned grid,
+                          unsigned rows, cudaStream_t st) {
+    using S = awq::kv::dec::Shape<D>;
+    auto kernel = awq::kv::dec::kv_decode_kernel<TQ, D>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, awq::kv::dec::THREADS, S::BYTES, st>>>(mk, mv, A);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    // the join starts beside the first kernel's end (programmatic dependent launch)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid, rows);
+    cfg.blockDim = dim3(128);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, awq::kv::dec::kv_decode_join_kernel<TQ, D>, (const awq::kv::dec::Args)A);
+}
+
 }  // namespace
 
 extern "C" {
@@ -211,8 +261,8 @@ awq_status awq_kv_append(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows k, 
 }
 
 size_t awq_kv_attention_workspace_bytes(awq_kv_cache c, int64_t T, int32_t q_heads, int32_t max_tokens) {
-    (void)c; (void)T; (void)q_heads; (void)max_tokens;
-    return 256;
+    if (T < 1 || q_heads < 1 || max_tokens < 1 || c.head_dim < 1) return 0;
+    return dec_ws(c.head_dim).total;
 }
 
 awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows q, awq_rows out, float scale,
@@ -222,14 +272,15 @@ awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows 
         (q.dtype != AWQ_F16 && q.dtype != AWQ_BF16) || out.dtype != q.dtype || q.heads != out.heads ||
         q.heads % c.heads || q.heads > 65535 || out.data == q.data)
         return AWQ_ERR_INVALID_ARG;
-    if (!(scale > 0.0f && scale <= 1e6f) || window < 0 || max_tokens < 1 || (!b.cu_tokens && max_tokens != 1))
+    if (!(scale > 0.0f && scale <= 1e6f) || window < 0 || max_tokens < 1 || (!b.cu_tokens && max_tokens != 1) ||
+        reinterpret_cast<uintptr_t>(lse) % 4)
         return AWQ_ERR_INVALID_ARG;
     if (!ws || ws_bytes < awq_kv_attention_workspace_bytes(c, T, q.heads, max_tokens) ||
         (reinterpret_cast<uintptr_t>(ws) & 255u))
         return AWQ_ERR_WORKSPACE;
     DevInfo d;
     if (awq_status e = device_info(d)) return e;
-    awq::kv::AttnArgs A;
+    awq::kv::dec::Args A;
     A.C = kv_cache(c);
     A.B = kv_batch(b);
     A.T = T;
@@ -238,16 +289,28 @@ awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows 
     A.scale_log2 = scale * 1.4426950408889634f;
     A.window = window;
     A.lse = lse;
+    A.group = q.heads / c.heads;
+    A.box_rows = c.page_size < awq::kv::dec::TILE ? c.page_size : awq::kv::dec::TILE;
+    const DecWs w = dec_ws(c.head_dim);
+    A.meta = static_cast<awq::kv::dec::Meta *>(ws);
+    A.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.ml_off);
+    A.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.o_off);
+    A.timeout_ns = (uint64_t)g_timeout_ms.load() * 1000000ull;
+    CUtensorMap mk, mv;
+    if (!encode_kv_map(&mk, c.k_codes, c, A.box_rows) || !encode_kv_map(&mv, c.v_codes, c, A.box_rows))
+        return AWQ_ERR_CUDA;
+    const unsigned grid = (unsigned)(2 * d.sms < kDecMaxGrid ? 2 * d.sms : kDecMaxGrid);
+    const int64_t most = (int64_t)max_tokens * A.group;
+    const unsigned rows = (unsigned)(most < awq::kv::dec::ROWS ? most : awq::kv::dec::ROWS);
     cudaStream_t st = (cudaStream_t)stream;
-    const dim3 grid((unsigned)T, (unsigned)q.heads);
-    const bool h = q.dtype == AWQ_F16;
-    if (c.head_dim == 64) {
-        if (h) awq::kv::attn_plain_kernel<__half, 64><<<grid, 128, 0, st>>>(A);
-        else awq::kv::attn_plain_kernel<__nv_bfloat16, 64><<<grid, 128, 0, st>>>(A);
-    } else {
-        if (h) awq::kv::attn_plain_kernel<__half, 128><<<grid, 128, 0, st>>>(A);
-        else awq::kv::attn_plain_kernel<__nv_bfloat16, 128><<<grid, 128, 0, st>>>(A);
-    }
+    cudaError_t e;
+    if (c.head_dim == 64)
+        e = q.dtype == AWQ_F16 ? launch_decode<__half, 64>(A, mk, mv, grid, rows, st)
+                               : launch_decode<__nv_bfloat16, 64>(A, mk, mv, grid, rows, st);
+    else
+        e = q.dtype == AWQ_F16 ? launch_decode<__half, 128>(A, mk, mv, grid, rows, st)
+                               : launch_decode<__nv_bfloat16, 128>(A, mk, mv, grid, rows, st);
+    if (e != cudaSuccess) return AWQ_ERR_CUDA;
     return last_launch();
 }
 
