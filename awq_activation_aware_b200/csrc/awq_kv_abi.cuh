@@ -108,24 +108,27 @@ bool encode_kv_map(CUtensorMap *m, const void *codes, const awq_kv_cache &c, int
               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Blocks of the decode attention: two an SM.
-constexpr int64_t kDecMaxGrid = 512;
+// Most blocks of the decode attention's first kernel, and rows of a tile.
+constexpr int64_t kDecMaxGrid = 512, kDecMaxRows = 16;
 struct DecWs {
     size_t ml_off, o_off, total;
 };
 DecWs dec_ws(int D) {
     DecWs w;
     w.ml_off = round_up(kDecMaxGrid * sizeof(awq::kv::dec::Meta), 256);
-    w.o_off = w.ml_off + round_up(kDecMaxGrid * 2 * awq::kv::dec::ROWS * 2 * 4, 256);
-    w.total = w.o_off + round_up((size_t)kDecMaxGrid * 2 * awq::kv::dec::ROWS * D * 4, 256);
+    w.o_off = w.ml_off + round_up(kDecMaxGrid * 2 * kDecMaxRows * 2 * 4, 256);
+    w.total = w.o_off + round_up((size_t)kDecMaxGrid * 2 * kDecMaxRows * D * 4, 256);
     return w;
 }
 
-template <typename TQ, int D>
-cudaError_t launch_decode(awq::kv::dec::Args &A, const CUtensorMap &mk, const CUtensorMap &mv, unsigned grid,
-                          unsigned rows, cudaStream_t st) {
-    using S = awq::kv::dec::Shape<D>;
-    auto kernel = awq::kv::dec::kv_decode_kernel<TQ, D>;
+template <typename TQ, int D, int NT>
+cudaError_t launch_decode_rows(awq::kv::dec::Args &A, const CUtensorMap &mk, const CUtensorMap &mv, int sms,
+                               int64_t most_rows, cudaStream_t st) {
+    using S = awq::kv::dec::Shape<D, NT>;
+    auto kernel = awq::kv::dec::kv_decode_kernel<TQ, D, NT>;
+    A.rows = S::ROWS;
+    const unsigned grid = (unsigned)std::min<int64_t>((int64_t)S::BLOCKS * sms, kDecMaxGrid);
+    const unsigned rows = (unsigned)std::min<int64_t>(most_rows, S::ROWS);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
     if (e != cudaSuccess) return e;
     kernel<<<grid, awq::kv::dec::THREADS, S::BYTES, st>>>(mk, mv, A);
@@ -141,6 +144,13 @@ cudaError_t launch_decode(awq::kv::dec::Args &A, const CUtensorMap &mk, const CU
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, awq::kv::dec::kv_decode_join_kernel<TQ, D>, (const awq::kv::dec::Args)A);
+}
+// Tiles of 8 query rows while a sequence has no more: half the products of 16.
+template <typename TQ, int D>
+cudaError_t launch_decode(awq::kv::dec::Args &A, const CUtensorMap &mk, const CUtensorMap &mv, int sms,
+                          int64_t most_rows, cudaStream_t st) {
+    if (most_rows <= 8) return launch_decode_rows<TQ, D, 1>(A, mk, mv, sms, most_rows, st);
+    return launch_decode_rows<TQ, D, 2>(A, mk, mv, sms, most_rows, st);
 }
 
 }  // namespace
@@ -299,17 +309,15 @@ awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows 
     CUtensorMap mk, mv;
     if (!encode_kv_map(&mk, c.k_codes, c, A.box_rows) || !encode_kv_map(&mv, c.v_codes, c, A.box_rows))
         return AWQ_ERR_CUDA;
-    const unsigned grid = (unsigned)(2 * d.sms < kDecMaxGrid ? 2 * d.sms : kDecMaxGrid);
     const int64_t most = (int64_t)max_tokens * A.group;
-    const unsigned rows = (unsigned)(most < awq::kv::dec::ROWS ? most : awq::kv::dec::ROWS);
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     if (c.head_dim == 64)
-        e = q.dtype == AWQ_F16 ? launch_decode<__half, 64>(A, mk, mv, grid, rows, st)
-                               : launch_decode<__nv_bfloat16, 64>(A, mk, mv, grid, rows, st);
+        e = q.dtype == AWQ_F16 ? launch_decode<__half, 64>(A, mk, mv, d.sms, most, st)
+                               : launch_decode<__nv_bfloat16, 64>(A, mk, mv, d.sms, most, st);
     else
-        e = q.dtype == AWQ_F16 ? launch_decode<__half, 128>(A, mk, mv, grid, rows, st)
-                               : launch_decode<__nv_bfloat16, 128>(A, mk, mv, grid, rows, st);
+        e = q.dtype == AWQ_F16 ? launch_decode<__half, 128>(A, mk, mv, d.sms, most, st)
+                               : launch_decode<__nv_bfloat16, 128>(A, mk, mv, d.sms, most, st);
     if (e != cudaSuccess) return AWQ_ERR_CUDA;
     return last_launch();
 }
