@@ -95,17 +95,35 @@ void launch_append(const awq::kv::AppendArgs &A, dim3 grid, cudaStream_t st) {
 
 // Codes as a 2-D tensor of bytes [n_pages * heads * page][D], boxes of `box_rows`
 // rows swizzled over their width.
-bool encode_kv_map(CUtensorMap *m, const void *codes, const awq_kv_cache &c, int box_rows) {
+bool encode_kv_map(CUtensorMap *m, const void *codes, const awq::kv::Cache &c, int box_rows) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)c.head_dim, (cuuint64_t)(c.n_pages * c.heads * c.page_size)};
-    cuuint64_t strides[1] = {(cuuint64_t)c.head_dim};
-    cuuint32_t box[2] = {(cuuint32_t)c.head_dim, (cuuint32_t)box_rows};
+    cuuint64_t dims[2] = {(cuuint64_t)c.dim, (cuuint64_t)(c.n_pages * c.heads * c.page)};
+    cuuint64_t strides[1] = {(cuuint64_t)c.dim};
+    cuuint32_t box[2] = {(cuuint32_t)c.dim, (cuuint32_t)box_rows};
     cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE,
-              c.head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A launch whose start may overlap the end of the kernel before it on the stream
+// (programmatic dependent launch): the kernel waits for that one (griddep_wait)
+// before it reads or writes anything in global memory, in every block of threads.
+template <typename... P>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, P... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
 // Most blocks of the decode attention's first kernel, and rows of a tile.
@@ -122,35 +140,35 @@ DecWs dec_ws(int D) {
 }
 
 template <typename TQ, int D, int NT>
-cudaError_t launch_decode_rows(awq::kv::dec::Args &A, const CUtensorMap &mk, const CUtensorMap &mv, int sms,
+cudaError_t launch_decode_rows(awq::kv::dec::Args &A, int sms,
                                int64_t most_rows, cudaStream_t st) {
     using S = awq::kv::dec::Shape<D, NT>;
     auto kernel = awq::kv::dec::kv_decode_kernel<TQ, D, NT>;
     A.rows = S::ROWS;
+    A.tile = S::TILE;
+    A.box_rows = std::min(A.C.page, S::TILE);
+    CUtensorMap mk, mv;
+    if (!encode_kv_map(&mk, A.C.codes[0], A.C, A.box_rows) || !encode_kv_map(&mv, A.C.codes[1], A.C, A.box_rows))
+        return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)std::min<int64_t>((int64_t)S::BLOCKS * sms, kDecMaxGrid);
     const unsigned rows = (unsigned)std::min<int64_t>(most_rows, S::ROWS);
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, awq::kv::dec::THREADS, S::BYTES, st>>>(mk, mv, A);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    // the join starts beside the first kernel's end (programmatic dependent launch)
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid, rows);
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, awq::kv::dec::kv_decode_join_kernel<TQ, D>, (const awq::kv::dec::Args)A);
+    A.rt_most = (int)((most_rows + S::ROWS - 1) / S::ROWS);
+    const int64_t segments = (int64_t)A.B.n_seqs * A.C.heads * A.rt_most;
+    A.by_segment = segments <= grid;
+    e = launch_overlapped(kernel, dim3(grid), awq::kv::dec::THREADS, S::BYTES, st, mk, mv, (const awq::kv::dec::Args)A);
+    if (e != cudaSuccess) return e;
+    return launch_overlapped(awq::kv::dec::kv_decode_join_kernel<TQ, D>,
+                             dim3(A.by_segment ? (unsigned)segments : grid, rows), 32 * awq::kv::dec::JOIN_WARPS, 0, st,
+                             (const awq::kv::dec::Args)A);
 }
 // Tiles of 8 query rows while a sequence has no more: half the products of 16.
 template <typename TQ, int D>
-cudaError_t launch_decode(awq::kv::dec::Args &A, const CUtensorMap &mk, const CUtensorMap &mv, int sms,
+cudaError_t launch_decode(awq::kv::dec::Args &A, int sms,
                           int64_t most_rows, cudaStream_t st) {
-    if (most_rows <= 8) return launch_decode_rows<TQ, D, 1>(A, mk, mv, sms, most_rows, st);
-    return launch_decode_rows<TQ, D, 2>(A, mk, mv, sms, most_rows, st);
+    if (most_rows <= 8) return launch_decode_rows<TQ, D, 1>(A, sms, most_rows, st);
+    return launch_decode_rows<TQ, D, 2>(A, sms, most_rows, st);
 }
 
 }  // namespace
@@ -300,24 +318,20 @@ awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows 
     A.window = window;
     A.lse = lse;
     A.group = q.heads / c.heads;
-    A.box_rows = c.page_size < awq::kv::dec::TILE ? c.page_size : awq::kv::dec::TILE;
     const DecWs w = dec_ws(c.head_dim);
     A.meta = static_cast<awq::kv::dec::Meta *>(ws);
     A.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.ml_off);
     A.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.o_off);
     A.timeout_ns = (uint64_t)g_timeout_ms.load() * 1000000ull;
-    CUtensorMap mk, mv;
-    if (!encode_kv_map(&mk, c.k_codes, c, A.box_rows) || !encode_kv_map(&mv, c.v_codes, c, A.box_rows))
-        return AWQ_ERR_CUDA;
     const int64_t most = (int64_t)max_tokens * A.group;
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     if (c.head_dim == 64)
-        e = q.dtype == AWQ_F16 ? launch_decode<__half, 64>(A, mk, mv, d.sms, most, st)
-                               : launch_decode<__nv_bfloat16, 64>(A, mk, mv, d.sms, most, st);
+        e = q.dtype == AWQ_F16 ? launch_decode<__half, 64>(A, d.sms, most, st)
+                               : launch_decode<__nv_bfloat16, 64>(A, d.sms, most, st);
     else
-        e = q.dtype == AWQ_F16 ? launch_decode<__half, 128>(A, mk, mv, d.sms, most, st)
-                               : launch_decode<__nv_bfloat16, 128>(A, mk, mv, d.sms, most, st);
+        e = q.dtype == AWQ_F16 ? launch_decode<__half, 128>(A, d.sms, most, st)
+                               : launch_decode<__nv_bfloat16, 128>(A, d.sms, most, st);
     if (e != cudaSuccess) return AWQ_ERR_CUDA;
     return last_launch();
 }

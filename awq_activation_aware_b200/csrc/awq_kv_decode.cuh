@@ -6,7 +6,7 @@
 // matters is that the codes stream without a pause and that the instructions to
 // turn them into operands fit beside the stream (an SM takes in 27 bytes a clock).
 //
-//  * Work.  A unit is 64 keys of one (sequence, key head, tile of 8 or 16 query rows); a
+//  * Work.  A unit is 64 keys (128 for D = 64) of one (sequence, key head, tile of 8 or 16 rows); a
 //    row is (new token, query head of the key head's group), so a group shares each
 //    key.  The units of a launch, in order, are cut into equal contiguous ranges,
 //    one per block of threads (two or three blocks an SM), whatever the lengths: a ragged
@@ -14,10 +14,13 @@
 //    device.  A segment (the units of one sequence, head and row tile) that crosses
 //    a cut leaves partial results, summed in order by a second kernel: the result
 //    does not depend on timing.
-//  * Stream.  One warp feeds a ring of stages by TMA, one box per page (64 keys at
-//    most), 128-byte rows swizzled (64-byte rows for D = 64), and the blocks' scales
-//    by 4-byte asynchronous copies.  Four warps consume: warp w owns keys
-//    16 w .. 16 w + 15 of each stage, one block of scales.
+//  * Stream.  One warp feeds a ring of 16 KB stages by TMA, one box per page (one unit
+//    at most), 128-byte rows swizzled (64-byte rows for D = 64), and the blocks' scales
+//    by 4-byte asynchronous copies; it reads 32 page numbers at a time, a batch ahead.
+//    Four warps consume, 32 keys (two blocks of scales) of a unit each, so for D = 128
+//    two of them every other unit: what a unit costs beside its keys (waits, masks,
+//    votes) is shared by more of them, and two chains of dependent instructions run
+//    side by side (342 instructions for 16 keys with one block at a time, 256 with two).
 //  * Products (mma m16n8k16, fp16 operands, binary32 sums), both with the codes as
 //    the 16-row operand: S^T = K Q^T and O^T = V^T P^T, so 8 query rows cost half of
 //    what 16 do and hold half the registers.  The codes are exact in fp16, and any
@@ -46,28 +49,32 @@ namespace awq {
 namespace kv {
 namespace dec {
 
-constexpr int TILE = 64;                   // keys per unit and stage
 constexpr int WARPS = 4;                   // consumer warps
 constexpr int THREADS = 32 * (WARPS + 1);
-constexpr float kLift = 9.0f, kSlack = 6.0f;
+constexpr float kLift = 9.0f, kSlack = 6.0f;       // see Scales above
 
 // NT tiles of 8 query rows.
 template <int D, int NT> struct Shape {
     static constexpr int ROWS = 8 * NT;
-    static constexpr int BLOCKS = NT == 1 ? 3 : 2;         // resident per SM
+    static constexpr int BLOCKS = NT == 1 ? 3 : 2;         // resident per SM: 128 or 168 registers a thread
+    static constexpr int TILE = 8192 / D;                  // keys per unit and stage
+    static constexpr int NB = TILE / kBlock;               // blocks of scales of a unit
+    static constexpr int TURNS = 2 * WARPS / NB;           // 32 keys a warp: every unit (D = 64), or every other
     static constexpr int STAGE = 2 * TILE * D;             // keys, values
-    static constexpr int STAGES = (NT == 1 ? 3 : 4) * (128 / D);
+    static constexpr int STAGES = 4;
+    static_assert(STAGES % TURNS == 0, "a stage's phases must all be waited for by the same warps");
     static constexpr int PER = D / 8;                      // elements of a row that one lane holds
     static constexpr int LD = D + 36;                      // row of the merge area: 4 floats after every PER, 4 more
-    static constexpr int OFF_SCALES = STAGES * STAGE;      // float [STAGES][8]
-    static constexpr int OFF_BARS = OFF_SCALES + STAGES * 32;
+    static constexpr int OFF_SCALES = STAGES * STAGE;      // float [STAGES][2 * NB]
+    static constexpr int OFF_BARS = OFF_SCALES + STAGES * 2 * NB * 4;
     static constexpr int OFF_ML = OFF_BARS + STAGES * 16;  // float [WARPS][ROWS][2]
     static constexpr int OFF_O = OFF_ML + WARPS * ROWS * 8;
-    static constexpr int BYTES = OFF_O + WARPS * ROWS * LD * 4 + 1024;   // + alignment
+    static constexpr int BYTES = OFF_O + ROWS * LD * 4 + 1024;     // + alignment
 };
 
-struct Meta {                              // a segment that starts in this block and ends in a later one
-    int32_t b, head, rt, last;             // last: the block of its last unit; -1: no such segment
+struct Meta {                              // a segment whose units lie in the ranges of several blocks
+    int32_t b, head, rt;
+    int32_t first, last;                   // the blocks of its first and last unit; last -1: no such segment
 };
 struct Args {
     Cache C;
@@ -78,9 +85,12 @@ struct Args {
     int64_t window;
     float *lse;
     int group;                             // query heads per key head
-    int rows;                              // query rows per tile: 8 or 16
-    int box_rows;                          // keys per TMA box: min(page, 64)
-    Meta *meta;                            // [grid]
+    int rows, tile;                        // query rows per tile, keys per unit
+    int box_rows;                          // keys per TMA box: min(page, tile)
+    // Where the join finds a split segment: by its own number (b heads + head) rt_most + rt while those are
+    // fewer than the blocks (by_segment), else by the block that starts it (at most one split segment each).
+    Meta *meta;
+    int by_segment, rt_most;
     float *part_ml;                        // [grid][2][rows][2]: slot 0 ends a segment begun earlier, slot 1 starts one
     float *part_o;                         // [grid][2][rows][D]
     uint64_t timeout_ns;
@@ -101,8 +111,8 @@ __device__ __forceinline__ Span span_of(const Args &A, int b) {
     p.hi = (int)(p.s.len < cap ? p.s.len : cap);
     const int64_t lo = A.window ? p.s.start + 1 - A.window : 0;
     p.lo = lo < 0 ? 0 : (lo > p.hi ? p.hi : (int)lo);
-    p.t0 = p.lo / TILE;
-    p.nt = (p.hi + TILE - 1) / TILE - p.t0;
+    p.t0 = p.lo / A.tile;
+    p.nt = (p.hi + A.tile - 1) / A.tile - p.t0;
     if (p.nt < 1) p.nt = 1;                // rows without keys still get their zeros
     p.rt = (int)(((int64_t)p.s.n * A.group + A.rows - 1) / A.rows);
     return p;
@@ -327,13 +337,14 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         abort_flag = 0;
         found[0] = found[1] = 0;
         for (int i = 0; i < S::STAGES; ++i) {
-            mbar_init(full + i, 16);
-            mbar_init(empty + i, WARPS);
+            mbar_init(full + i, 4 * S::NB);
+            mbar_init(empty + i, S::NB / 2);
         }
         fence_mbar_init();
-        A.meta[blockIdx.x].last = -1;
     }
     griddep_launch_dependents();
+    griddep_wait();                        // everything above runs beside the end of the kernel before
+    if (threadIdx.x == 0 && !A.by_segment) A.meta[blockIdx.x].last = -1;
     __syncthreads();
     const Range R = find_range(A, sums, found);
     if (R.first >= R.end) return;
@@ -341,51 +352,62 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     cur.start(A, R);
 
     if (warp == WARPS) {
-        // ---- the stream: lanes 0-7 a box of keys or values each, lanes 8-15 a block's scale each
-        const int which = (lane >> 2) & 1, j = lane & 3;
-        const int rows = lane < 8 ? A.box_rows : kBlock;           // keys this lane looks after
-        const bool active = lane < 8 ? j < TILE / A.box_rows : lane < 16;
+        // ---- the stream: 2 NB lanes for boxes of keys or values, 2 NB lanes for the blocks' scales
+        const int which = (lane / S::NB) & 1, j = lane % S::NB;
+        const bool boxes = lane < 2 * S::NB, mine = lane < 4 * S::NB;
+        const int rows = boxes ? A.box_rows : kBlock;              // keys this lane looks after
+        const bool active = mine && j * rows < S::TILE;
         const void *tmap = which ? &tmap_v : &tmap_k;
-        auto page_at = [&](int64_t u) -> int64_t {                 // -1: nothing there; -2: a bad page
-            const int pos = (cur.p.t0 + (int)(u - cur.seg0)) * TILE + j * rows;
-            if (!active || pos >= cur.p.hi) return -1;
-            const int64_t p = A.B.pages[(int64_t)cur.b * A.B.ld_pages + pos / A.C.page];
-            return p < 0 || p >= A.C.n_pages ? -2 : p;
+        const int page_bits = 31 - __clz(A.C.page);
+        // page numbers: entries [32 k, 32 k + 32) of a sequence's row, one a lane.  A unit's never straddle two batches.
+        auto fetch = [&](int b, int k) -> int32_t {
+            const int64_t i = (int64_t)k * 32 + lane;
+            return i < A.B.max_pages ? A.B.pages[(int64_t)b * A.B.ld_pages + i] : -1;
         };
+        auto batch_of = [&](int64_t u) { return ((cur.p.t0 + (int)(u - cur.seg0)) * S::TILE >> page_bits) >> 5; };
         if (lane == 0 && cur.p.s.len > cur.p.hi) atomicOr(&g_dev_error, kDevErrBadIndex);
-        int64_t page = page_at(cur.u);
+        int hold_b = cur.b, hold_k = batch_of(R.first);
+        int32_t hold = fetch(hold_b, hold_k), ahead = fetch(hold_b, hold_k + 1);
         int stage = 0;
         uint32_t phase = 1;                                        // the first round finds the stages empty
         int64_t issued = 0;
         bool ok = true;
         for (int64_t u = R.first; u < R.end; ++u) {
-            const int pos = (cur.p.t0 + (int)(u - cur.seg0)) * TILE + j * rows;
-            const int64_t tile = (page * A.C.heads + cur.head) * A.C.page + pos % A.C.page;      // its first row
-            const int64_t here = page;
-            if (u + 1 < R.end) {                                   // the next page number is on its way meanwhile
+            const int pos = (cur.p.t0 + (int)(u - cur.seg0)) * S::TILE + j * rows, head = cur.head;
+            int64_t page = __shfl_sync(0xffffffffu, hold, (pos >> page_bits) & 31);
+            if (!active || pos >= cur.p.hi) page = -1;             // nothing there
+            else if (page < 0 || page >= A.C.n_pages) page = -2;   // a bad page
+            if (u + 1 < R.end) {                                   // the next unit's page numbers are on their way meanwhile
                 if (u + 1 == cur.seg_end()) {
                     cur.next(A);
                     if (lane == 0 && cur.p.s.len > cur.p.hi) atomicOr(&g_dev_error, kDevErrBadIndex);
                 }
-                page = page_at(u + 1);
+                const int k = batch_of(u + 1);
+                if (cur.b != hold_b || k != hold_k) {
+                    hold = cur.b == hold_b && k == hold_k + 1 ? ahead : fetch(cur.b, k);
+                    ahead = fetch(cur.b, k + 1);
+                    hold_b = cur.b;
+                    hold_k = k;
+                }
             }
-            ok = mbar_wait_warp(empty + stage, phase, &abort_flag, A.timeout_ns);
+            ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty + stage, phase, &abort_flag, A.timeout_ns));
             if (!ok) break;
-            if (lane < 8) {
-                if (here >= 0) {
+            const int64_t tile = (page * A.C.heads + head) * A.C.page + (pos & (A.C.page - 1));  // its first row
+            if (boxes) {
+                if (page >= 0) {
                     mbar_arrive_expect_tx(full + stage, rows * D);
-                    tma_load_2d(sm + stage * S::STAGE + which * TILE * D + j * rows * D, tmap, 0, (int32_t)tile, full + stage);
+                    tma_load_2d(sm + stage * S::STAGE + (which * S::TILE + j * rows) * D, tmap, 0, (int32_t)tile, full + stage);
                 } else {
                     mbar_arrive(full + stage);
                 }
-            } else if (lane < 16) {
-                float *dst = scales + stage * 8 + which * 4 + j;
-                if (here >= 0) {
+            } else if (mine) {
+                float *dst = scales + (stage * 2 + which) * S::NB + j;
+                if (page >= 0) {
                     cp_async_4(dst, A.C.scales[which] + tile / kBlock);
                     cp_async_arrive_noinc(full + stage);
                 } else {
                     *dst = -1.0f;                                  // no such block
-                    if (here == -2) atomicOr(&g_dev_error, kDevErrBadIndex);
+                    if (page == -2) atomicOr(&g_dev_error, kDevErrBadIndex);
                     mbar_arrive(full + stage);
                 }
             }
@@ -407,178 +429,223 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         return;
     }
 
-    // ---- consumers
-    const int g = lane >> 2, c = lane & 3;
+    // ---- consumers: 32 keys of a unit each; TURNS = 2: warps 0, 1 every other unit, warps 2, 3 the ones between
+    const int g = lane >> 2, c = lane & 3, part = warp % (S::NB / 2);
     constexpr int NJ = D / 16;                                     // 16-row tiles of the second product
+    constexpr int KB = NT == 1 ? 2 : 1;                            // blocks of 16 keys taken at once (registers)
     uint32_t qf[NT][D / 16][2];
-    float rowf[NT][2], base[NT][2], l[NT][2], o[NT][NJ][4];        // base: m - kLift of rows 2 c, 2 c + 1 of a tile
+    float rowf[NT][2], base[NT][2], l[NT][2], o[NT][NJ][4];        // base: m - kLift of rows 2 c, 2 c + 1 of a tile,
+    uint32_t has = 0;                                              // once they saw a key (bit 2 t + x), else 0
+    bool settled = false;                                          // every row of the warp has
     int pos_of[NT][2];                                             // their positions
-    int all_lo = 0, all_hi = 0;                                    // keys that every row of the tile sees
     int stage = 0;
     uint32_t phase = 0;
-    bool fresh = true, ok = true;
-    for (int64_t u = R.first; u < R.end; ++u) {
-        if (fresh) {
-            fresh = false;
-            const int n = cur.p.s.n, row0 = cur.rt * ROWS;
+    bool ok = true;
+    for (int64_t done = R.first; done < R.end;) {
+        // ---- a segment, or this block's part of it
+        const int n = cur.p.s.n, row0 = cur.rt * ROWS;
+        int all_lo, all_hi;                                        // keys that every row of the tile sees
+        {
             int last = (row0 + ROWS - 1) / A.group;
             if (last >= n) last = n - 1;
             const int64_t p0 = cur.p.s.start + row0 / A.group + 1, p1 = cur.p.s.start + last + 1 - A.window;
             all_hi = p0 < 0 ? 0 : (p0 < cur.p.hi ? (int)p0 : cur.p.hi);
             all_lo = A.window && p1 > 0 ? (p1 < kMaxLen ? (int)p1 : (int)kMaxLen) : 0;
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float unscale = load_query<TQ, D>(A, cur, row0 + 8 * t + g, qf[t]) * A.scale_log2;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    rowf[t][x] = __shfl_sync(0xffffffffu, unscale, 4 * (2 * c + x));       // from the lane that loaded the row
-                    base[t][x] = -INFINITY;
-                    l[t][x] = 0.0f;
-                    int i = (row0 + 8 * t + 2 * c + x) / A.group;
-                    if (i >= n) i = n - 1;                         // rows of nobody follow the last token
-                    const int64_t at = cur.p.s.start + i;
-                    pos_of[t][x] = at < kMaxLen ? (at < -1 ? -1 : (int)at) : (int)kMaxLen;
-                }
-#pragma unroll
-                for (int j = 0; j < NJ; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
-            }
         }
-        // a wait that ran out skips the keys but not the barriers below
-        ok = ok && mbar_wait_warp(full + stage, phase, &abort_flag, A.timeout_ns);
-        const int key0 = (cur.p.t0 + (int)(u - cur.seg0)) * TILE + 16 * warp;
-        const int left = cur.p.hi - key0;                          // keys of the block that exist
-        const float ks = scales[stage * 8 + warp], vs = scales[stage * 8 + 4 + warp];
-        if (ok && left > 0 && ks >= 0.0f && vs >= 0.0f) {
-            const uint32_t kt = smem_u32(sm + stage * S::STAGE), vt = kt + TILE * D;
-            float s[NT][4];                                        // keys g (0, 1), g + 8 (2, 3) of rows 2 c, 2 c + 1
 #pragma unroll
-            for (int t = 0; t < NT; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.0f;
+        for (int t = 0; t < NT; ++t) {
+            const float unscale = load_query<TQ, D>(A, cur, row0 + 8 * t + g, qf[t]) * A.scale_log2;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const uint4 k0 = lds128(kt + chunk_at<D>(16 * warp + g, (D / 64) * c + i));
-                const uint4 k1 = lds128(kt + chunk_at<D>(16 * warp + 8 + g, (D / 64) * c + i));
-                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const uint32_t a[4] = {cvt_lo(w0[j]), cvt_lo(w1[j]), cvt_hi(w0[j]), cvt_hi(w1[j])};
-#pragma unroll
-                    for (int t = 0; t < NT; ++t) mma_16816(s[t], a, qf[t][4 * i + j][0], qf[t][4 * i + j][1]);
-                }
+            for (int x = 0; x < 2; ++x) {
+                rowf[t][x] = __shfl_sync(0xffffffffu, unscale, 4 * (2 * c + x));           // from the lane that loaded the row
+                base[t][x] = 0.0f;
+                l[t][x] = 0.0f;
+                int i = (row0 + 8 * t + 2 * c + x) / A.group;
+                if (i >= n) i = n - 1;                             // rows of nobody follow the last token
+                const int64_t at = cur.p.s.start + i;
+                pos_of[t][x] = at < kMaxLen ? (at < -1 ? -1 : (int)at) : (int)kMaxLen;
             }
-            const int e = exponent_of(vs);
-            const float ev = (float)e, inv_v = pow2(-e);
-            const bool whole = key0 >= all_lo && key0 + 16 <= all_hi;
-            // x + e; hidden keys -inf
-            float top = -INFINITY;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float f0 = rowf[t][0] * ks, f1 = rowf[t][1] * ks;
-                s[t][0] = __fmaf_rn(s[t][0], f0, ev);
-                s[t][1] = __fmaf_rn(s[t][1], f1, ev);
-                s[t][2] = __fmaf_rn(s[t][2], f0, ev);
-                s[t][3] = __fmaf_rn(s[t][3], f1, ev);
-                if (!whole) {
+            for (int j = 0; j < NJ; ++j) o[t][j][0] = o[t][j][1] = o[t][j][2] = o[t][j][3] = 0.0f;
+        }
+        has = 0;
+        settled = false;
+        const int units = (int)((cur.seg_end() < R.end ? cur.seg_end() : R.end) - done);
+        int first_key = (cur.p.t0 + (int)(done - cur.seg0)) * S::TILE + 32 * part;
+        int turn = (int)((done - R.first) & 1);
+        for (int left = units; left > 0; --left, first_key += S::TILE, turn ^= 1) {
+            if (S::TURNS == 1 || turn == warp / 2) {
+                // a wait that ran out skips the keys but not the barriers below
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(full + stage, phase, &abort_flag, A.timeout_ns));
+#pragma unroll 1
+              for (int b0 = 0; b0 < 2; b0 += KB) {
+                const int key0 = first_key + 16 * b0;
+                float ks[KB], vs[KB];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int key = key0 + g + 8 * (k >> 1), at = pos_of[t][k & 1];
-                        if (key > at || key >= cur.p.hi || (A.window && key <= at - A.window)) s[t][k] = -INFINITY;
-                    }
+                for (int b = 0; b < KB; ++b) {
+                    ks[b] = scales[stage * 2 * S::NB + 2 * part + b0 + b];
+                    vs[b] = scales[stage * 2 * S::NB + S::NB + 2 * part + b0 + b];
                 }
-                // past base + kLift + kSlack? (a row without a reference: past -inf)
-                top = fmaxf(top, fmaxf(fmaxf(s[t][0], s[t][2]) - base[t][0], fmaxf(s[t][1], s[t][3]) - base[t][1]));
-            }
-            if (__any_sync(0xffffffffu, top > kLift + kSlack)) {   // seldom: raise the references
+                const uint32_t kt = smem_u32(sm + stage * S::STAGE) + (32 * part + 16 * b0) * D, vt = kt + S::TILE * D;
+                const bool whole = key0 >= all_lo && key0 + 16 * KB <= all_hi && fminf(ks[0], ks[KB - 1]) >= 0.0f;
+                if (ok && (whole || key0 < cur.p.hi)) {
+                    float s[KB][NT][4];                            // keys g (0, 1), g + 8 (2, 3) of rows 2 c, 2 c + 1
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                    for (int b = 0; b < KB; ++b)
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        float mx = fmaxf(s[t][x], s[t][2 + x]);
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16)) - kLift;
-                        const float f = mx > base[t][x] ? ex2(base[t][x] - mx) : 1.0f;
-                        base[t][x] = fmaxf(mx, base[t][x]);
-                        l[t][x] *= f;
+                        for (int t = 0; t < NT; ++t) s[b][t][0] = s[b][t][1] = s[b][t][2] = s[b][t][3] = 0.0f;
 #pragma unroll
-                        for (int j = 0; j < NJ; ++j) {
-                            o[t][j][x] *= f;
-                            o[t][j][2 + x] *= f;
+                    for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+                        for (int b = 0; b < KB; ++b) {
+                            const uint4 k0 = lds128(kt + chunk_at<D>(16 * b + g, (D / 64) * c + i));
+                            const uint4 k1 = lds128(kt + chunk_at<D>(16 * b + 8 + g, (D / 64) * c + i));
+                            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t a[4] = {cvt_lo(w0[j]), cvt_lo(w1[j]), cvt_hi(w0[j]), cvt_hi(w1[j])};
+#pragma unroll
+                                for (int t = 0; t < NT; ++t) mma_16816(s[b][t], a, qf[t][4 * i + j][0], qf[t][4 * i + j][1]);
+                            }
+                        }
+                    // z = x + e - base, hidden keys -inf; 2^e = the value scale, inv_v = 2^-e
+                    float top = -INFINITY, inv_v[KB];
+#pragma unroll
+                    for (int b = 0; b < KB; ++b) {
+                        const uint32_t bits = __float_as_uint(vs[b]);
+                        const float ev = __fsub_rn(__uint_as_float(0x4b400000u + (bits >> 23)), kMagic + 127.0f);
+                        inv_v[b] = __uint_as_float(0x7f000000u - bits);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            const float f0 = rowf[t][0] * ks[b], f1 = rowf[t][1] * ks[b];
+                            const float c0 = ev - base[t][0], c1 = ev - base[t][1];
+                            s[b][t][0] = __fmaf_rn(s[b][t][0], f0, c0);
+                            s[b][t][1] = __fmaf_rn(s[b][t][1], f1, c1);
+                            s[b][t][2] = __fmaf_rn(s[b][t][2], f0, c0);
+                            s[b][t][3] = __fmaf_rn(s[b][t][3], f1, c1);
+                            if (!whole) {
+                                const bool none = ks[b] < 0.0f;        // a block that is not there
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int key = key0 + 16 * b + g + 8 * (k >> 1), at = pos_of[t][k & 1];
+                                    if (none || key > at || key >= cur.p.hi || (A.window && key <= at - A.window))
+                                        s[b][t][k] = -INFINITY;
+                                }
+                            }
+                            top = fmax3(fmax3(top, s[b][t][0], s[b][t][1]), s[b][t][2], s[b][t][3]);
                         }
                     }
-            }
-            uint32_t pb[NT][2];
+                    if (!settled || __any_sync(0xffffffffu, top > kLift + kSlack)) {       // seldom: raise the references
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const float b0 = base[t][0] == -INFINITY ? 0.0f : base[t][0];
-                const float b1 = base[t][1] == -INFINITY ? 0.0f : base[t][1];
+                        for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) s[t][k] = ex2(s[t][k] - (k & 1 ? b1 : b0));
-                l[t][0] = __fmaf_rn(s[t][0] + s[t][2], inv_v, l[t][0]);
-                l[t][1] = __fmaf_rn(s[t][1] + s[t][3], inv_v, l[t][1]);
-                pb[t][0] = transpose8x8(pack_f16(s[t][0], s[t][1]));       // keys 2 c, 2 c + 1 of row g
-                pb[t][1] = transpose8x8(pack_f16(s[t][2], s[t][3]));       // keys 2 c + 8, 2 c + 9
-            }
-            // values of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9: D / 8 codes of each
-            uint32_t v[4][D / 32];
+                            for (int x = 0; x < 2; ++x) {
+                                float mx = fmaxf(fmaxf(s[0][t][x], s[0][t][2 + x]), fmaxf(s[KB - 1][t][x], s[KB - 1][t][2 + x]));
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                                const uint32_t bit = 1u << (2 * t + x);
+                                float up = 0.0f, f = 1.0f;
+                                if (has & bit) {
+                                    up = fmaxf(mx - kLift, 0.0f);
+                                    f = ex2(-up);
+                                } else if (mx > -INFINITY) {
+                                    up = mx - kLift;               // the row's first keys: its sums are still 0
+                                    has |= bit;
+                                }
+                                base[t][x] += up;
+                                l[t][x] *= f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t row = 16 * warp + 2 * c + (k & 1) + 8 * (k >> 1);
-                if constexpr (D == 128) {
-                    const uint4 x = lds128(vt + chunk_at<D>(row, g));
-                    v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
-                } else {
-                    const uint2 x = lds64(vt + chunk_at<D>(row, g >> 1) + (g & 1) * 8);
-                    v[k][0] = x.x; v[k][1] = x.y;
-                }
-            }
-            if (!whole) {
-                // keys that do not exist: zeros.  NaN codes: zeros here, NaN in the sums of the rows that see them.
-                uint32_t bad = 0;                                  // bit i: key i of the 16
+                                for (int j = 0; j < NJ; ++j) {
+                                    o[t][j][x] *= f;
+                                    o[t][j][2 + x] *= f;
+                                }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int key = 2 * c + (k & 1) + 8 * (k >> 1);
+                                for (int b = 0; b < KB; ++b) {
+                                    s[b][t][x] -= up;
+                                    s[b][t][2 + x] -= up;
+                                }
+                            }
+                        settled = __all_sync(0xffffffffu, has == (1u << (2 * NT)) - 1);
+                    }
+                    uint32_t pb[KB][NT][2];
 #pragma unroll
-                    for (int w = 0; w < D / 32; ++w) {
-                        if (key >= left) v[k][w] = 0;
-                        const uint32_t n = nan_bytes(v[k][w]);
-                        if (n) {
-                            bad |= 1u << key;
-                            v[k][w] &= ~((n >> 7) * 0xffu);
+                    for (int b = 0; b < KB; ++b)
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) s[b][t][k] = ex2(s[b][t][k]);
+                            l[t][0] = __fmaf_rn(s[b][t][0] + s[b][t][2], inv_v[b], l[t][0]);
+                            l[t][1] = __fmaf_rn(s[b][t][1] + s[b][t][3], inv_v[b], l[t][1]);
+                            pb[b][t][0] = transpose8x8(pack_f16(s[b][t][0], s[b][t][1]));  // keys 2 c, 2 c + 1 of row g
+                            pb[b][t][1] = transpose8x8(pack_f16(s[b][t][2], s[b][t][3]));  // keys 2 c + 8, 2 c + 9
+                        }
+#pragma unroll
+                    for (int b = 0; b < KB; ++b) {
+                        // values of keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9: D / 8 codes of each
+                        uint32_t v[4][D / 32];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const uint32_t row = 16 * b + 2 * c + (k & 1) + 8 * (k >> 1);
+                            if constexpr (D == 128) {
+                                const uint4 x = lds128(vt + chunk_at<D>(row, g));
+                                v[k][0] = x.x; v[k][1] = x.y; v[k][2] = x.z; v[k][3] = x.w;
+                            } else {
+                                const uint2 x = lds64(vt + chunk_at<D>(row, g >> 1) + (g & 1) * 8);
+                                v[k][0] = x.x; v[k][1] = x.y;
+                            }
+                        }
+                        if (!whole) {
+                            // keys that do not exist: zeros.  NaN codes: zeros here, NaN in the sums of the rows that see them.
+                            const int exist = ks[b] < 0.0f ? 0 : cur.p.hi - (key0 + 16 * b);
+                            uint32_t bad = 0;                      // bit i: key i of the 16
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int key = 2 * c + (k & 1) + 8 * (k >> 1);
+#pragma unroll
+                                for (int w = 0; w < D / 32; ++w) {
+                                    if (key >= exist) v[k][w] = 0;
+                                    const uint32_t nan = nan_bytes(v[k][w]);
+                                    if (nan) {
+                                        bad |= 1u << key;
+                                        v[k][w] &= ~((nan >> 7) * 0xffu);
+                                    }
+                                }
+                            }
+                            bad = __reduce_or_sync(0xffffffffu, bad);
+#pragma unroll
+                            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const int i = g + 8 * (k >> 1), key = key0 + 16 * b + i, at = pos_of[t][k & 1];
+                                    if (((bad >> i) & 1) && key <= at && (!A.window || key > at - A.window)) l[t][k & 1] = NAN;
+                                }
+                        }
+#pragma unroll
+                        for (int w = 0; w < D / 32; ++w) {
+                            const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
+                            const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
+                            const uint32_t a0[4] = {cvt_lo(x0), cvt_hi(x0), cvt_lo(y0), cvt_hi(y0)};   // elements 4 w, 4 w + 1
+                            const uint32_t a1[4] = {cvt_lo(x1), cvt_hi(x1), cvt_lo(y1), cvt_hi(y1)};   // elements 4 w + 2, 4 w + 3
+#pragma unroll
+                            for (int t = 0; t < NT; ++t) {
+                                mma_16816(o[t][2 * w], a0, pb[b][t][0], pb[b][t][1]);
+                                mma_16816(o[t][2 * w + 1], a1, pb[b][t][0], pb[b][t][1]);
+                            }
                         }
                     }
                 }
-                bad = __reduce_or_sync(0xffffffffu, bad);
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int i = g + 8 * (k >> 1), key = key0 + i, at = pos_of[t][k & 1];
-                        if (((bad >> i) & 1) && key <= at && (!A.window || key > at - A.window)) l[t][k & 1] = NAN;
-                    }
+              }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + stage);
             }
-#pragma unroll
-            for (int w = 0; w < D / 32; ++w) {
-                const uint32_t x0 = __byte_perm(v[0][w], v[1][w], 0x5140), x1 = __byte_perm(v[0][w], v[1][w], 0x7362);
-                const uint32_t y0 = __byte_perm(v[2][w], v[3][w], 0x5140), y1 = __byte_perm(v[2][w], v[3][w], 0x7362);
-                const uint32_t a0[4] = {cvt_lo(x0), cvt_hi(x0), cvt_lo(y0), cvt_hi(y0)};   // elements 4 w, 4 w + 1
-                const uint32_t a1[4] = {cvt_lo(x1), cvt_hi(x1), cvt_lo(y1), cvt_hi(y1)};   // elements 4 w + 2, 4 w + 3
-#pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    mma_16816(o[t][2 * w], a0, pb[t][0], pb[t][1]);
-                    mma_16816(o[t][2 * w + 1], a1, pb[t][0], pb[t][1]);
-                }
+            if (++stage == S::STAGES) {
+                stage = 0;
+                phase ^= 1;
             }
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + stage);
-        if (++stage == S::STAGES) {
-            stage = 0;
-            phase ^= 1;
-        }
-
-        if (u + 1 < R.end && u + 1 < cur.seg_end()) continue;
-        // ---- the segment, or this block's part of it, is done: join the four warps
-        fresh = true;
+        done += units;
+        // ---- join the four warps: each brings its sums to the common reference and adds them in turn
         float *ml = reinterpret_cast<float *>(sm + S::OFF_ML), *oa = reinterpret_cast<float *>(sm + S::OFF_O);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -588,39 +655,55 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 sum += __shfl_xor_sync(0xffffffffu, sum, 4);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                const int r = warp * ROWS + 8 * t + 2 * c + x;
                 if (g == 0) {
-                    ml[2 * r] = base[t][x];
-                    ml[2 * r + 1] = sum;
+                    float *p = ml + (warp * ROWS + 8 * t + 2 * c + x) * 2;
+                    p[0] = (has >> (2 * t + x)) & 1 ? base[t][x] : -INFINITY;
+                    p[1] = sum;
                 }
-                float *row = oa + r * S::LD + g * (S::PER + 4);
-#pragma unroll
-                for (int j = 0; j < NJ; j += 2)
-                    *reinterpret_cast<float4 *>(row + 2 * j) =
-                        make_float4(o[t][j][x], o[t][j][2 + x], o[t][j + 1][x], o[t][j + 1][2 + x]);
             }
         consumers_sync();
+        auto common = [&](int r) {
+            return fmaxf(fmaxf(ml[2 * r], ml[2 * (ROWS + r)]), fmaxf(ml[2 * (2 * ROWS + r)], ml[2 * (3 * ROWS + r)]));
+        };
+        for (int w = 0; w < WARPS; ++w) {
+            if (w == warp) {
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        const int r = 8 * t + 2 * c + x;
+                        const float f = (has >> (2 * t + x)) & 1 ? ex2(base[t][x] - common(r)) : 0.0f;
+                        float *row = oa + r * S::LD + g * (S::PER + 4);
+#pragma unroll
+                        for (int j = 0; j < NJ; j += 2) {
+                            float4 *p = reinterpret_cast<float4 *>(row + 2 * j);
+                            float4 v = w ? *p : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            v.x = __fmaf_rn(f, o[t][j][x], v.x);
+                            v.y = __fmaf_rn(f, o[t][j][2 + x], v.y);
+                            v.z = __fmaf_rn(f, o[t][j + 1][x], v.z);
+                            v.w = __fmaf_rn(f, o[t][j + 1][2 + x], v.w);
+                            *p = v;
+                        }
+                    }
+            }
+            consumers_sync();
+        }
         const bool begins = cur.seg0 >= R.first, ends = cur.seg_end() <= R.end;
         const int tid = threadIdx.x;
         for (int i = tid; i < ROWS * D / 8; i += 32 * WARPS) {
             const int r = i / (D / 8), d = (i % (D / 8)) * 8;
             const int row = cur.rt * ROWS + r, tok = row / A.group, hq = cur.head * A.group + row % A.group;
             if (tok >= cur.p.s.n) continue;
-            float mx = -INFINITY, L = 0.0f, v[8] = {};
-#pragma unroll
-            for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, ml[(w * ROWS + r) * 2]);
+            const float mx = common(r);
+            float L = 0.0f;
 #pragma unroll
             for (int w = 0; w < WARPS; ++w) {
-                const float mw = ml[(w * ROWS + r) * 2], lw = ml[(w * ROWS + r) * 2 + 1];
-                const float f = mw == -INFINITY ? 1.0f : ex2(mw - mx);      // without keys all is 0 (or NaN)
-                L = __fmaf_rn(f, lw, L);
-                const float4 *p = reinterpret_cast<const float4 *>(oa + (w * ROWS + r) * S::LD + d + 4 * (d / S::PER));
-                const float4 x = p[0], y = p[1];
-                v[0] = __fmaf_rn(f, x.x, v[0]); v[1] = __fmaf_rn(f, x.y, v[1]);
-                v[2] = __fmaf_rn(f, x.z, v[2]); v[3] = __fmaf_rn(f, x.w, v[3]);
-                v[4] = __fmaf_rn(f, y.x, v[4]); v[5] = __fmaf_rn(f, y.y, v[5]);
-                v[6] = __fmaf_rn(f, y.z, v[6]); v[7] = __fmaf_rn(f, y.w, v[7]);
+                const float mw = ml[(w * ROWS + r) * 2];
+                if (mw > -INFINITY) L = __fmaf_rn(ex2(mw - mx), ml[(w * ROWS + r) * 2 + 1], L);
             }
+            const float4 *p = reinterpret_cast<const float4 *>(oa + r * S::LD + d + 4 * (d / S::PER));
+            const float4 a = p[0], b = p[1];
+            float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
             if (begins && ends) {
                 const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
@@ -639,60 +722,101 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 }
             }
         }
-        if (begins && !ends && tid == 0) {
+        if (begins && tid == 0 && (A.by_segment || !ends)) {
             // the block of the segment's last unit x: the last i with total i / blocks <= x
-            A.meta[blockIdx.x] = {cur.b, cur.head, cur.rt, (int32_t)((cur.seg_end() * R.blocks - 1) / R.total)};
+            const int64_t last = ends ? -1 : (cur.seg_end() * R.blocks - 1) / R.total;
+            A.meta[A.by_segment ? (cur.b * A.C.heads + cur.head) * A.rt_most + cur.rt : (int)blockIdx.x] =
+                {cur.b, cur.head, cur.rt, (int32_t)blockIdx.x, (int32_t)last};
         }
         consumers_sync();
-        if (u + 1 < R.end) cur.next(A);
+        if (done < R.end) cur.next(A);
     }
 }
 
-// One block of threads per (block of the first kernel, row): the segment that
-// starts there, its parts summed in order.  Four warps take every fourth part.
+// One block of threads per (split segment, row): its parts, summed in order.  Eight
+// warps take every eighth part; all of a warp's loads are on their way together.
+constexpr int JOIN_WARPS = 8;
 template <typename TQ, int D>
-__global__ void __launch_bounds__(128) kv_decode_join_kernel(const Args A) {
-    constexpr int N = D / 32;
-    const int ROWS = A.rows;
-    __shared__ float sl[4], so[4][D];
+__global__ void __launch_bounds__(32 * JOIN_WARPS) kv_decode_join_kernel(const Args A) {
+    constexpr int N = D / 32, DEEP = 8;
+    __shared__ float sl[JOIN_WARPS], so[JOIN_WARPS][D];
+    griddep_launch_dependents();
     griddep_wait();
-    const Meta M = A.meta[blockIdx.x];
-    if (M.last < 0) return;
-    const Seq s = seq_info(A.B, M.b, A.T);
-    const int r = blockIdx.y, row = M.rt * ROWS + r, tok = row / A.group, hq = M.head * A.group + row % A.group;
+    const int r = blockIdx.y;
+    Meta M;
+    Seq s;
+    if (A.by_segment) {
+        const int rt = blockIdx.x % A.rt_most, bh = blockIdx.x / A.rt_most;
+        s = seq_info(A.B, bh / A.C.heads, A.T);                    // beside the load of M
+        M = A.meta[blockIdx.x];
+        if ((int64_t)rt * A.rows >= (int64_t)s.n * A.group) return;      // there is no such segment
+        if (M.last < 0) return;
+    } else {
+        M = A.meta[blockIdx.x];
+        if (M.last < 0) return;
+        s = seq_info(A.B, M.b, A.T);
+    }
+    const int row = M.rt * A.rows + r, tok = row / A.group, hq = M.head * A.group + row % A.group;
     if (tok >= s.n) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int first = blockIdx.x;
-    auto slot_of = [&](int i) { return ((int64_t)i * 2 + (i == first ? 1 : 0)) * ROWS + r; };
-    // the largest maximum over all parts, then this warp's sums relative to it
-    float mx = -INFINITY;
-    for (int i = first + lane; i <= M.last; i += 32) mx = fmaxf(mx, A.part_ml[slot_of(i) * 2]);
+    auto slot_of = [&](int i) { return ((int64_t)i * 2 + (i == M.first ? 1 : 0)) * A.rows + r; };
+    float mx = -INFINITY, L = 0.0f, v[N] = {};                     // mx: reference of L and v
+    for (int i0 = M.first + warp; i0 <= M.last; i0 += JOIN_WARPS * DEEP) {
+        float2 p[DEEP];
+        float x[DEEP][N];
 #pragma unroll
-    for (int k = 16; k; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-    float L = 0.0f, v[N] = {};
-#pragma unroll 4
-    for (int i = first + warp; i <= M.last; i += 4) {
-        const int64_t at = slot_of(i);
-        const float2 p = *reinterpret_cast<const float2 *>(A.part_ml + at * 2);
-        float x[N];
-        load_n(A.part_o + at * D + lane * N, x);
-        const float f = p.x == -INFINITY ? 1.0f : ex2(p.x - mx);
-        L = __fmaf_rn(f, p.y, L);
+        for (int k = 0; k < DEEP; ++k) {
+            const int i = i0 + k * JOIN_WARPS;
+            p[k] = make_float2(-INFINITY, 0.0f);
+            if (i <= M.last) {
+                p[k] = *reinterpret_cast<const float2 *>(A.part_ml + slot_of(i) * 2);
+                load_n(A.part_o + slot_of(i) * D + lane * N, x[k]);
+            }
+        }
+        float top = mx;
 #pragma unroll
-        for (int k = 0; k < N; ++k) v[k] = __fmaf_rn(f, x[k], v[k]);
+        for (int k = 0; k < DEEP; ++k) top = fmaxf(top, p[k].x);
+        if (top == -INFINITY) continue;
+        const float f0 = ex2(mx - top);
+        L *= f0;
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] *= f0;
+#pragma unroll
+        for (int k = 0; k < DEEP; ++k)
+            if (p[k].x > -INFINITY) {
+                const float f = ex2(p[k].x - top);
+                L = __fmaf_rn(f, p[k].y, L);
+#pragma unroll
+                for (int n = 0; n < N; ++n) v[n] = __fmaf_rn(f, x[k][n], v[n]);
+            }
+        mx = top;
     }
-    if (lane == 0) sl[warp] = L;
+    __shared__ float sm[JOIN_WARPS];
+    if (lane == 0) {
+        sm[warp] = mx;
+        sl[warp] = L;
+    }
 #pragma unroll
-    for (int k = 0; k < N; ++k) so[warp][lane * N + k] = v[k];
+    for (int n = 0; n < N; ++n) so[warp][lane * N + n] = v[n];
     __syncthreads();
     if (warp) return;
-    L = (sl[0] + sl[1]) + (sl[2] + sl[3]);
+    mx = sm[0];
+#pragma unroll
+    for (int w = 1; w < JOIN_WARPS; ++w) mx = fmaxf(mx, sm[w]);
+    L = 0.0f;
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = 0.0f;
+#pragma unroll
+    for (int w = 0; w < JOIN_WARPS; ++w)
+        if (sm[w] > -INFINITY) {
+            const float f = ex2(sm[w] - mx);
+            L = __fmaf_rn(f, sl[w], L);
+#pragma unroll
+            for (int n = 0; n < N; ++n) v[n] = __fmaf_rn(f, so[w][lane * N + n], v[n]);
+        }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int d = lane * N + k;
-        v[k] = ((so[0][d] + so[1][d]) + (so[2][d] + so[3][d])) * inv;
-    }
+    for (int n = 0; n < N; ++n) v[n] *= inv;
     store_n(static_cast<TQ *>(const_cast<void *>(A.out.data)) + (int64_t)(s.row0 + tok) * A.out.ld_tok +
                 (int64_t)hq * A.out.ld_head + lane * N, v);
     if (A.lse && lane == 0)
