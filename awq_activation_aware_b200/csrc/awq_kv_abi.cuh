@@ -126,6 +126,20 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Runs `set` the first time it is reached on the current device (one flag per use of a lambda type).
+template <typename F>
+cudaError_t once_per_device(F set) {
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= 64) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+    if (!done[dev].load(std::memory_order_acquire)) {
+        if ((e = set()) != cudaSuccess) return e;
+        done[dev].store(true, std::memory_order_release);
+    }
+    return cudaSuccess;
+}
+
 // Most blocks of the decode attention's first kernel, and rows of a tile.
 constexpr int64_t kDecMaxGrid = 512, kDecMaxRows = 16;
 struct DecWs {
@@ -152,7 +166,9 @@ cudaError_t launch_decode_rows(awq::kv::dec::Args &A, int sms,
         return cudaErrorInvalidValue;
     const unsigned grid = (unsigned)std::min<int64_t>((int64_t)S::BLOCKS * sms, kDecMaxGrid);
     const unsigned rows = (unsigned)std::min<int64_t>(most_rows, S::ROWS);
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    cudaError_t e = once_per_device([&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    });
     if (e != cudaSuccess) return e;
     A.rt_most = (int)((most_rows + S::ROWS - 1) / S::ROWS);
     const int64_t segments = (int64_t)A.B.n_seqs * A.C.heads * A.rt_most;

@@ -60,9 +60,15 @@ def declare(L):
         getattr(L, fn).restype = ctypes.c_int
 
 
+_loaded = None
+
+
 def _lib():
-    from . import lib
-    return lib()
+    global _loaded
+    if _loaded is None:
+        from . import lib
+        _loaded = lib()
+    return _loaded
 
 
 def _check(code, where):
@@ -77,90 +83,111 @@ def _enter(device, stream):
         yield
 
 
-def _on(device: torch.device, stream):
+_HERE = contextlib.nullcontext()
+
+
+def _on(device: int, stream):
     """Context for a call on `device`: the tensors' device current, and memory
     that the call allocates taken on the stream that uses it."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return _enter(device, stream)
+    return _HERE if stream is None and device == torch.cuda.current_device() else _enter(device, stream)
 
 
-def _raw_stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+def _raw_stream(stream, device: int) -> int:
+    # the bare handle: current_stream() builds an object, which costs more than a small kernel
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
-def _rows(t: torch.Tensor, name: str, device=None) -> Rows:
+def _where(t, device: int, name: str):
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
+
+
+def _rows(t: torch.Tensor, name: str, device: int) -> Rows:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.stride(2) != 1:
-        raise ValueError(f"{name} must be [tokens, heads, head_dim] with contiguous elements")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim]")
     T, H, D = t.shape
-    return Rows(t.data_ptr(), t.stride(0) if T > 1 else H * D, t.stride(1) if H > 1 else D, H, code)
+    tok, head, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name} must have contiguous elements")
+    if t.get_device() != device:
+        _where(t, device, name)
+    return Rows(t.data_ptr(), tok if T > 1 else H * D, head if H > 1 else D, H, code)
 
 
-def _ints(t: torch.Tensor, name: str, device, shape) -> int:
+def _cuda(t, name: str) -> int:
+    """The device of a CUDA tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _ints(t: torch.Tensor, name: str, device: int, n: int) -> int:
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32:
         raise TypeError(f"{name} must be an int32 CUDA tensor")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous of shape {shape}, got {tuple(t.shape)}")
+    if t.get_device() != device:
+        _where(t, device, name)
+    if t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous of shape {(n,)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
-def _cache(c: dict, device) -> KVCache:
+def _cache(c: dict, device: int, D: int) -> KVCache:
     k, v, ks, vs = c["k_codes"], c["v_codes"], c["k_scales"], c["v_scales"]
     if k.dim() != 4 or v.shape != k.shape:
         raise ValueError("k_codes and v_codes must be [pages, heads, page, head_dim] alike")
-    n, H, P, D = k.shape
-    for t, name in ((k, "k_codes"), (v, "v_codes")):
-        if t.dtype not in _CODES:
-            raise TypeError(f"{name} must be float8_e4m3fn, got {t.dtype}")
-    for t, name in ((ks, "k_scales"), (vs, "v_scales")):
-        if t.dtype != torch.float32:
-            raise TypeError(f"{name} must be float32, got {t.dtype}")
-        if tuple(t.shape) != (n, H, P // 16):
-            raise ValueError(f"{name} must be {(n, H, P // 16)}, got {tuple(t.shape)}")
+    n, H, P, dim = k.shape
+    if dim != D:
+        raise ValueError(f"head_dim {D}, the cache's is {dim}")
+    if k.dtype not in _CODES or v.dtype not in _CODES:
+        raise TypeError(f"k_codes and v_codes must be float8_e4m3fn, got {k.dtype} and {v.dtype}")
+    if ks.dtype != torch.float32 or vs.dtype != torch.float32:
+        raise TypeError(f"k_scales and v_scales must be float32, got {ks.dtype} and {vs.dtype}")
+    if ks.shape != (n, H, P // 16) or vs.shape != ks.shape:
+        raise ValueError(f"k_scales and v_scales must be {(n, H, P // 16)}, got {tuple(ks.shape)} and {tuple(vs.shape)}")
     for t in (k, v, ks, vs):
-        if t.device != device:
-            raise ValueError(f"the cache is on {t.device}, expected {device}")
+        if t.get_device() != device:
+            _where(t, device, "the cache")
         if not t.is_contiguous():
             raise ValueError("the cache's tensors must be contiguous")
     return KVCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n, P, H, D)
 
 
-def _batch(seq_lens, pages, cu_tokens, T, device) -> KVBatch:
+def _batch(seq_lens, pages, cu_tokens, T, device: int) -> KVBatch:
     if not isinstance(pages, torch.Tensor) or pages.dim() != 2 or pages.dtype != torch.int32:
         raise TypeError("pages must be an int32 CUDA tensor [sequences, pages]")
-    if pages.device != device:
-        raise ValueError(f"pages is on {pages.device}, expected {device}")
+    if pages.get_device() != device:
+        _where(pages, device, "pages")
     n, width = pages.shape
-    if width < 1 or (width > 1 and pages.stride(1) != 1) or (n > 1 and pages.stride(0) < width):
+    row, one = pages.stride()
+    if n == 1:
+        row = width
+    if width < 1 or (width > 1 and one != 1) or row < width:
         raise ValueError("pages must have at least one column and contiguous rows that do not overlap")
-    lens = _ints(seq_lens, "seq_lens", device, (n,))
+    lens = _ints(seq_lens, "seq_lens", device, n)
     cu = None
     if cu_tokens is not None:
-        cu = _ints(cu_tokens, "cu_tokens", device, (n + 1,))
+        cu = _ints(cu_tokens, "cu_tokens", device, n + 1)
     elif T != n:
         raise ValueError(f"without cu_tokens every sequence has one new token: {T} rows, {n} sequences")
-    return KVBatch(lens, cu, pages.data_ptr(), n, pages.stride(0) if n > 1 else width, width)
+    return KVBatch(lens, cu, pages.data_ptr(), n, row, width)
 
 
-def _rope_cfg(table, layout, device) -> RopeCfg:
-    if layout not in _LAYOUTS:
+def _rope_cfg(table, layout, device: int) -> RopeCfg:
+    code = _LAYOUTS.get(layout)
+    if code is None:
         raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")
     if not isinstance(table, torch.Tensor) or table.dtype != torch.float32 or not table.is_cuda:
         raise TypeError("table must be a float32 CUDA tensor")
     if table.dim() != 3 or table.shape[2] != 2 or not table.is_contiguous():
         raise ValueError("table must be contiguous [positions, rot_dim / 2, 2], as rope_table returns it")
-    if table.device != device:
-        raise ValueError(f"table is on {table.device}, expected {device}")
-    return RopeCfg(table.data_ptr(), table.shape[0], 2 * table.shape[1], _LAYOUTS[layout])
+    if table.get_device() != device:
+        _where(table, device, "table")
+    n, half, _ = table.shape
+    return RopeCfg(table.data_ptr(), n, 2 * half, code)
 
 
 def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: str | None = None, factor: float = 1.0,
@@ -176,12 +203,11 @@ def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: str | N
     device = torch.device(device)
     if device.type != "cuda":
         raise TypeError("the table lives on a CUDA device")
-    if device.index is None:
-        device = torch.device("cuda", torch.cuda.current_device())
+    index = torch.cuda.current_device() if device.index is None else device.index
     sc = RopeScaling(_SCALINGS[scaling], factor, original, beta_fast, beta_slow, magnitude)
-    with _on(device, stream):
-        t = torch.empty((n_pos, rot_dim // 2, 2), dtype=torch.float32, device=device)
-        _check(_lib().awq_rope_table(n_pos, rot_dim, base, sc, t.data_ptr(), _raw_stream(stream, device)),
+    with _on(index, stream):
+        t = torch.empty((n_pos, rot_dim // 2, 2), dtype=torch.float32, device=torch.device("cuda", index))
+        _check(_lib().awq_rope_table(n_pos, rot_dim, base, sc, t.data_ptr(), _raw_stream(stream, index)),
                "awq_rope_table")
     return t
 
@@ -191,14 +217,14 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: 
     """Rotary positions of x [T, heads, head_dim]: pair i of the first rot_dim elements turns by its row's angle
     (positions int32 [T]); the rest is copied.  The result has x's type, or `dtype`, or goes to `out` (x itself:
     in place).  inverse=True applies the transpose, which is the gradient: dx = rope(dy, ..., inverse=True)."""
-    xr = _rows(x, "x")
-    device = x.device
+    device = _cuda(x, "x")
+    xr = _rows(x, "x", device)
     T, H, D = x.shape
-    pos = _ints(positions, "positions", device, (T,))
+    pos = _ints(positions, "positions", device, T)
     cfg = _rope_cfg(table, layout, device)
     with _on(device, stream):
         if out is None:
-            out = torch.empty((T, H, D), dtype=x.dtype if dtype is None else dtype, device=device)
+            out = torch.empty((T, H, D), dtype=x.dtype if dtype is None else dtype, device=x.device)
         elif out.shape != x.shape or (dtype is not None and out.dtype != dtype):
             raise ValueError("out must have x's shape and the asked type")
         if T == 0:
@@ -227,14 +253,12 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Ten
     seq_lens int32 [n]: tokens of each sequence, the new ones included; pages int32 [n, max_pages]; cu_tokens
     int32 [n + 1]: the new tokens' rows of each sequence (None: row b is sequence b's one new token).  With q
     (k's type) its rotated rows are returned, in q_dtype or in q_out; otherwise None."""
-    kr, vr = _rows(k, "k"), _rows(v, "v", k.device)
-    device = k.device
+    device = _cuda(k, "k")
+    kr, vr = _rows(k, "k", device), _rows(v, "v", device)
     T, H, D = k.shape
     if v.shape != k.shape:
         raise ValueError("k and v must have one shape")
-    if cache["k_codes"].shape[-1] != D:
-        raise ValueError(f"head_dim {D}, the cache's is {cache['k_codes'].shape[-1]}")
-    C = _cache(cache, device)
+    C = _cache(cache, device, D)
     B = _batch(seq_lens, pages, cu_tokens, T, device)
     cfg = RopeCfg() if table is None else _rope_cfg(table, layout, device)
     if q is not None and table is None:
@@ -246,7 +270,7 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Ten
             if q.shape[0] != T or q.shape[2] != D:
                 raise ValueError("q must have k's tokens and head_dim")
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q_dtype, device=device)
+                q_out = torch.empty(q.shape, dtype=q_dtype, device=k.device)
             elif q_out.shape != q.shape:
                 raise ValueError("q_out must have q's shape")
             qo = _rows(q_out, "q_out", device)
@@ -269,23 +293,21 @@ def kv_attention(cache: dict, q: torch.Tensor, seq_lens: torch.Tensor, pages: to
     own keys appended before.  seq_lens, pages and cu_tokens as in kv_append; max_tokens bounds the new tokens of
     any sequence.  scale defaults to head_dim^-0.5; window > 0 hides keys that far back.  Rows that see no key
     give 0.  Returns out [T, q_heads, head_dim], with return_lse also the float32 log-sum-exp [T, q_heads]."""
-    qr = _rows(q, "q")
-    device = q.device
+    device = _cuda(q, "q")
+    qr = _rows(q, "q", device)
     T, H, D = q.shape
-    if cache["k_codes"].shape[-1] != D:
-        raise ValueError(f"head_dim {D}, the cache's is {cache['k_codes'].shape[-1]}")
-    C = _cache(cache, device)
+    C = _cache(cache, device, D)
     B = _batch(seq_lens, pages, cu_tokens, T, device)
     L = _lib()
     with _on(device, stream):
         if out is None:
-            out = torch.empty((T, H, D), dtype=q.dtype, device=device)
+            out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
         elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
-        lse = torch.empty((T, H), dtype=torch.float32, device=device) if return_lse else None
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
         if T:
             need = L.awq_kv_attention_workspace_bytes(C, T, H, max_tokens)
-            ws = torch.empty(need, dtype=torch.uint8, device=device) if workspace is None else workspace
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device) if workspace is None else workspace
             _check(L.awq_kv_attention(C, B, T, qr, _rows(out, "out", device),
                                       1.0 / math.sqrt(D) if scale is None else scale, max_tokens, window,
                                       lse.data_ptr() if return_lse else None, ws.data_ptr(), ws.numel(),
@@ -308,7 +330,7 @@ def attention_step(x: torch.Tensor, qkv: dict, o: dict, cache: dict, seq_lens: t
         raise ValueError(f"qkv has {qkv['codes'].shape[0]} rows, {q_heads} + 2 x {heads} heads of {D} need "
                          f"{(q_heads + 2 * heads) * D}")
     T = x.shape[0]
-    with _on(x.device, stream):
+    with _on(_cuda(x, "x"), stream):
         y = qlinear(qkv["codes"], qkv["scales"], qkv["zeros"], qkv["s_best"], x, bits, group, stream=stream)
         y = y.view(T, q_heads + 2 * heads, D)
         q, k, v = y[:, :q_heads], y[:, q_heads:q_heads + heads], y[:, q_heads + heads:]
