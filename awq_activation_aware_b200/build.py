@@ -18,7 +18,7 @@ CSRC = PKG / "csrc"
 LIB = PKG / "libawq.so"
 SOURCES = [CSRC / "awq_abi.cu"]
 DEPS = SOURCES + [CSRC / "awq_kernels.cuh", CSRC / "awq_device.cuh", CSRC / "awq_kv.cuh",
-                  CSRC / "awq_kv_decode.cuh", CSRC / "awq_kv_abi.cuh", ROOT / "include" / "awq.h"]
+                  CSRC / "awq_kv_decode.cuh", CSRC / "awq_kv_prefill.cuh", CSRC / "awq_kv_abi.cuh", ROOT / "include" / "awq.h"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",

@@ -16,6 +16,7 @@
 #include "awq_kernels.cuh"
 #include "awq_kv.cuh"
 #include "awq_kv_decode.cuh"
+#include "awq_kv_prefill.cuh"
 
 namespace {
 

@@ -59,7 +59,8 @@ struct Seq {
     int64_t start;             // may be negative: those rows have no place in the cache
     int64_t len;               // start + n
 };
-__device__ __forceinline__ Seq seq_info(const Batch &B, int b, int64_t T) {
+// A sequence with more new tokens than `most` is an error: it is reported and has none.
+__device__ __forceinline__ Seq seq_info(const Batch &B, int b, int64_t T, int most = 0x7fffffff) {
     Seq s;
     int64_t r0 = b, r1 = b + 1;
     if (B.cu) {
@@ -71,6 +72,10 @@ __device__ __forceinline__ Seq seq_info(const Batch &B, int b, int64_t T) {
     if (r1 > T) r1 = T;
     s.row0 = (int)r0;
     s.n = r1 > r0 ? (int)(r1 - r0) : 0;
+    if (s.n > most) {
+        atomicOr(&g_dev_error, kDevErrBadIndex);
+        s.n = 0;
+    }
     const int64_t len = B.seq_lens[b];
     s.len = len < 0 ? 0 : len;
     s.start = s.len - s.n;

@@ -187,6 +187,56 @@ cudaError_t launch_decode(awq::kv::dec::Args &A, int sms,
     return launch_decode_rows<TQ, D, 2>(A, sms, most_rows, st);
 }
 
+// The kernel for many rows: blocks of threads, and splits of the keys while they do not fill the machine.
+constexpr int64_t kPreSplitBlocks = 148;
+int64_t pre_items(const awq::kv::Batch &B, const awq::kv::Cache &C, int64_t most_rows) {
+    return (int64_t)B.n_seqs * C.heads * ((most_rows + awq::kv::pre::ROWS - 1) / awq::kv::pre::ROWS);
+}
+size_t pre_ml_bytes() { return kPreSplitBlocks * awq::kv::pre::ROWS * 2 * 4; }
+size_t pre_ws(int D) { return pre_ml_bytes() + (size_t)kPreSplitBlocks * awq::kv::pre::ROWS * D * 4; }
+
+template <typename TQ, int D>
+cudaError_t launch_prefill(const awq::kv::dec::Args &P, int64_t most_rows, void *ws, cudaStream_t st) {
+    using S = awq::kv::pre::Shape<D>;
+    auto kernel = awq::kv::pre::kv_prefill_kernel<TQ, D>;
+    cudaError_t e = once_per_device([&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    });
+    if (e != cudaSuccess) return e;
+    const int64_t items = pre_items(P.B, P.C, most_rows);
+    const int64_t key_tiles = (P.B.max_pages * P.C.page + awq::kv::pre::TILE - 1) / awq::kv::pre::TILE;
+    const int64_t splits = std::max<int64_t>(1, std::min(kPreSplitBlocks / items, key_tiles / 2));
+    if (items * splits > kMaxDim) return cudaErrorInvalidConfiguration;
+    awq::kv::pre::Args A;
+    A.C = P.C;
+    A.B = P.B;
+    A.T = P.T;
+    A.q = P.q;
+    A.out = P.out;
+    A.scale_log2 = P.scale_log2;
+    A.window = P.window;
+    A.lse = P.lse;
+    A.group = P.group;
+    A.splits = (int)splits;
+    A.max_tokens = P.max_tokens;
+    A.part_ml = static_cast<float *>(ws);
+    A.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + pre_ml_bytes());
+    A.timeout_ns = P.timeout_ns;
+    e = launch_overlapped(kernel, dim3((unsigned)(items * splits)), awq::kv::pre::THREADS, S::BYTES, st,
+                          (const awq::kv::pre::Args)A);
+    if (e != cudaSuccess || splits == 1) return e;
+    const int64_t warps = P.T * P.q.heads;
+    return launch_overlapped(awq::kv::pre::kv_prefill_join_kernel<TQ, D>, dim3((unsigned)((warps + 7) / 8)), 256, 0, st,
+                             (const awq::kv::pre::Args)A);
+}
+// Up to kDecRows rows of a sequence and key head the kernel for few rows, from there on the other.
+constexpr int64_t kDecRows = 16;
+template <typename TQ, int D>
+cudaError_t launch_attention(awq::kv::dec::Args &A, int sms, int64_t most_rows, void *ws, cudaStream_t st) {
+    if (most_rows <= kDecRows) return launch_decode<TQ, D>(A, sms, most_rows, st);
+    return launch_prefill<TQ, D>(A, most_rows, ws, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -306,7 +356,8 @@ awq_status awq_kv_append(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows k, 
 
 size_t awq_kv_attention_workspace_bytes(awq_kv_cache c, int64_t T, int32_t q_heads, int32_t max_tokens) {
     if (T < 1 || q_heads < 1 || max_tokens < 1 || c.head_dim < 1) return 0;
-    return dec_ws(c.head_dim).total;
+    const int64_t rows = c.heads < 1 ? 1 : (int64_t)max_tokens * (q_heads / c.heads);
+    return rows <= kDecRows ? dec_ws(c.head_dim).total : pre_ws(c.head_dim);
 }
 
 awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows q, awq_rows out, float scale,
@@ -317,7 +368,7 @@ awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows 
         q.heads % c.heads || q.heads > 65535 || out.data == q.data)
         return AWQ_ERR_INVALID_ARG;
     if (!(scale > 0.0f && scale <= 1e6f) || window < 0 || max_tokens < 1 || (!b.cu_tokens && max_tokens != 1) ||
-        reinterpret_cast<uintptr_t>(lse) % 4)
+        reinterpret_cast<uintptr_t>(lse) % 4 || T > kMaxDim / (2 * q.heads) || max_tokens > kMaxDim / (2 * q.heads))
         return AWQ_ERR_INVALID_ARG;
     if (!ws || ws_bytes < awq_kv_attention_workspace_bytes(c, T, q.heads, max_tokens) ||
         (reinterpret_cast<uintptr_t>(ws) & 255u))
@@ -334,6 +385,7 @@ awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows 
     A.window = window;
     A.lse = lse;
     A.group = q.heads / c.heads;
+    A.max_tokens = max_tokens;
     const DecWs w = dec_ws(c.head_dim);
     A.meta = static_cast<awq::kv::dec::Meta *>(ws);
     A.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.ml_off);
@@ -343,11 +395,11 @@ awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows 
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     if (c.head_dim == 64)
-        e = q.dtype == AWQ_F16 ? launch_decode<__half, 64>(A, d.sms, most, st)
-                               : launch_decode<__nv_bfloat16, 64>(A, d.sms, most, st);
+        e = q.dtype == AWQ_F16 ? launch_attention<__half, 64>(A, d.sms, most, ws, st)
+                               : launch_attention<__nv_bfloat16, 64>(A, d.sms, most, ws, st);
     else
-        e = q.dtype == AWQ_F16 ? launch_decode<__half, 128>(A, d.sms, most, st)
-                               : launch_decode<__nv_bfloat16, 128>(A, d.sms, most, st);
+        e = q.dtype == AWQ_F16 ? launch_attention<__half, 128>(A, d.sms, most, ws, st)
+                               : launch_attention<__nv_bfloat16, 128>(A, d.sms, most, ws, st);
     if (e != cudaSuccess) return AWQ_ERR_CUDA;
     return last_launch();
 }

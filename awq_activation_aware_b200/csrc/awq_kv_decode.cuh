@@ -90,7 +90,7 @@ struct Args {
     // Where the join finds a split segment: by its own number (b heads + head) rt_most + rt while those are
     // fewer than the blocks (by_segment), else by the block that starts it (at most one split segment each).
     Meta *meta;
-    int by_segment, rt_most;
+    int by_segment, rt_most, max_tokens;
     float *part_ml;                        // [grid][2][rows][2]: slot 0 ends a segment begun earlier, slot 1 starts one
     float *part_o;                         // [grid][2][rows][D]
     uint64_t timeout_ns;
@@ -105,7 +105,7 @@ struct Span {
 constexpr int64_t kMaxLen = 1 << 30;       // positions fit 32 bits with room to spare
 __device__ __forceinline__ Span span_of(const Args &A, int b) {
     Span p;
-    p.s = seq_info(A.B, b, A.T);
+    p.s = seq_info(A.B, b, A.T, A.max_tokens);
     int64_t cap = A.B.max_pages * A.C.page;
     if (cap > kMaxLen) cap = kMaxLen;
     p.hi = (int)(p.s.len < cap ? p.s.len : cap);
@@ -747,14 +747,14 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_decode_join_kernel(const A
     Seq s;
     if (A.by_segment) {
         const int rt = blockIdx.x % A.rt_most, bh = blockIdx.x / A.rt_most;
-        s = seq_info(A.B, bh / A.C.heads, A.T);                    // beside the load of M
+        s = seq_info(A.B, bh / A.C.heads, A.T, A.max_tokens);                    // beside the load of M
         M = A.meta[blockIdx.x];
         if ((int64_t)rt * A.rows >= (int64_t)s.n * A.group) return;      // there is no such segment
         if (M.last < 0) return;
     } else {
         M = A.meta[blockIdx.x];
         if (M.last < 0) return;
-        s = seq_info(A.B, M.b, A.T);
+        s = seq_info(A.B, M.b, A.T, A.max_tokens);
     }
     const int row = M.rt * A.rows + r, tok = row / A.group, hq = M.head * A.group + row % A.group;
     if (tok >= s.n) return;

@@ -1,0 +1,570 @@
+// Attention over the paged 8-bit cache for many query rows per key head: prompts,
+// chunks of prompts and longer drafts (sm_100a).  See awq_kv.cuh for the cache.
+//
+// The products bound it (tcgen05, fp16 operands, binary32 accumulators in tensor
+// memory): 4 D operations a (row, key).  A block of threads owns 256 query rows, two
+// tiles of 128, of one sequence and key head -- a row is (new token, query head of the
+// key head's group), so a group shares each key -- and runs over the keys 128 at a time:
+//
+//   warps 0-3, 4-7   softmax of tile 0, tile 1: one row a thread.  Scores S from tensor
+//                    memory, P' = 2^(x + e - base) as fp16 back into the columns S came
+//                    from, the row's sum and reference in registers.
+//   warps 8-11       codes to fp16 operands: 16 codes a load, one tile ahead in
+//                    registers, exact conversion, 128-byte-swizzled tiles in shared
+//                    memory.  One conversion serves 256 rows.
+//   warp 12          one thread issues the products: S = Q K^T from shared memory,
+//                    O += P' V with P' from tensor memory and V [key][D] as it lies in
+//                    the cache (the operand whose rows run along D).
+//
+// While one tile's softmax runs the tensor core works for the other.  Scales and
+// references are those of the kernel for few rows (awq_kv_decode.cuh): the key scale
+// multiplies the score, the value scale is an exponent, a row's reference is raised
+// only when a score passes it by 2^6, and then its part of O is rescaled in tensor
+// memory; O's products of the step before are done by then, since they were issued
+// before the scores whose completion the softmax waited for.
+//
+// With too few blocks of rows to fill the machine the keys are split over several
+// blocks of threads, and a second kernel joins their parts in order.
+#pragma once
+
+#include "awq_kv_decode.cuh"
+
+namespace awq {
+namespace kv {
+namespace pre {
+
+using dec::cvt_hi;
+using dec::cvt_lo;
+using dec::ex2;
+using dec::kLift;
+using dec::kMaxLen;
+using dec::kSlack;
+using dec::nan_bytes;
+using dec::pack_f16;
+
+constexpr int ROWS = 256, TILE = 128;      // query rows and keys per step of a block of threads
+constexpr int SOFT_WARPS = 8, CONV_WARP = 8, MMA_WARP = 12;
+constexpr int THREADS = 32 * 13;
+constexpr int SLOTS = 4;                   // tiles whose scales are kept
+
+template <int D> struct Shape {
+    static constexpr int OPERAND = TILE * D * 2;           // one tile of Q, K or V as fp16
+    static constexpr int OFF_Q = 0, OFF_K = 2 * OPERAND, OFF_V = 4 * OPERAND;
+    static constexpr int OFF_SC = 6 * OPERAND;             // float4 [SLOTS][8]: key scale, e, 2^-e of a block's values
+    static constexpr int OFF_NAN = OFF_SC + SLOTS * 8 * 16;        // byte [SLOTS][TILE]: the key's values hold a NaN
+    static constexpr int OFF_BAR = OFF_NAN + SLOTS * TILE;
+    static constexpr int BYTES = OFF_BAR + 256 + 1024;     // + alignment
+};
+
+struct Args {
+    Cache C;
+    Batch B;
+    int64_t T;
+    Rows q, out;
+    float scale_log2;
+    int64_t window;
+    float *lse;
+    int group, splits, max_tokens;
+    float *part_ml;                        // [block][ROWS][2]
+    float *part_o;                         // [block][ROWS][D]
+    uint64_t timeout_ns;
+};
+
+// What a block of threads works on.  Blocks that have the most keys come first.
+struct Item {
+    Seq s;
+    int b, head, split;
+    int row0, rows;                        // first row, rows of the sequence and head
+    int hi;                                // keys that exist for some row
+    int t0, nt;                            // first tile of keys, and how many (of this split)
+    int all_lo, all_hi;                    // keys that every row sees
+    bool any;
+};
+__device__ __forceinline__ int clamp_pos(int64_t p) { return p < 0 ? 0 : (p < kMaxLen ? (int)p : (int)kMaxLen); }
+__device__ __forceinline__ Item item_of(const Args &A, int64_t i) {
+    Item w;
+    w.split = (int)(i % A.splits);
+    i /= A.splits;
+    w.head = (int)(i % A.C.heads);
+    i /= A.C.heads;
+    w.b = (int)(i % A.B.n_seqs);
+    const int64_t from_end = i / A.B.n_seqs;
+    w.s = seq_info(A.B, w.b, A.T, A.max_tokens);
+    w.rows = w.s.n * A.group;
+    const int tiles = (w.rows + ROWS - 1) / ROWS;
+    w.any = from_end < tiles;
+    if (!w.any) return w;
+    w.row0 = (int)(tiles - 1 - from_end) * ROWS;
+    const int first = w.row0 / A.group;
+    int last = (w.row0 + ROWS - 1) / A.group;
+    if (last >= w.s.n) last = w.s.n - 1;
+    int64_t cap = A.B.max_pages * A.C.page;
+    if (cap > kMaxLen) cap = kMaxLen;
+    if (w.s.len < cap) cap = w.s.len;
+    const int64_t hi = w.s.start + last + 1, lo = A.window ? w.s.start + first + 1 - A.window : 0;
+    w.hi = clamp_pos(hi < cap ? hi : cap);
+    w.t0 = clamp_pos(lo) / TILE;
+    int nt = (w.hi + TILE - 1) / TILE - w.t0;
+    if (nt < 0) nt = 0;
+    const int per = (nt + A.splits - 1) / A.splits;
+    const int j0 = w.split * per;
+    w.t0 += j0;
+    w.nt = nt - j0 < per ? nt - j0 : per;
+    if (w.nt < 0) w.nt = 0;
+    w.all_hi = clamp_pos(w.s.start + first + 1);
+    if (w.all_hi > w.hi) w.all_hi = w.hi;
+    w.all_lo = A.window ? clamp_pos(w.s.start + last + 1 - A.window) : 0;
+    return w;
+}
+__device__ __forceinline__ bool whole_tile(const Item &w, int key0) { return key0 >= w.all_lo && key0 + TILE <= w.all_hi; }
+
+// Descriptor of an operand whose 16-bit elements run along its M or N rows ([k][64] tiles of
+// 128-byte rows, swizzled): 8 k 1024 bytes apart, the next 64 elements `leading` bytes on.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t leading) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(leading >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+// One tile's scores of one row, all 128: P' packed, block sums into `add` (scaled by 2^-e), the largest
+// z = x + e - base.  MASKED: keys outside [lo, hi) of the tile are hidden.
+template <bool MASKED>
+__device__ __forceinline__ void soft_tile(uint32_t s_tmem, const float4 *sc, float rowf, float base, int lo, int hi,
+                                          uint32_t (&p)[TILE / 2], float &add, float &top) {
+    add = 0.0f;
+    top = -INFINITY;
+#pragma unroll
+    for (int ch = 0; ch < 4; ++ch) {
+        float v[32];
+        tmem_ld_32x32b_x32_sync(s_tmem + 32 * ch, v);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+            const float4 q = sc[2 * ch + b];
+            const float2 f = make_float2(rowf * q.x, rowf * q.x), c = make_float2(q.y - base, q.y - base);
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+                const int i = 16 * b + k;
+                float2 z = fma2_rn(make_float2(v[i], v[i + 1]), f, c);
+                if (MASKED) {
+                    const int key = 32 * ch + i;
+                    if (key < lo || key >= hi) z.x = -INFINITY;
+                    if (key + 1 < lo || key + 1 >= hi) z.y = -INFINITY;
+                }
+                top = fmax3(top, z.x, z.y);
+                z.x = ex2(z.x);
+                z.y = ex2(z.y);
+                sum = __fadd2_rn(sum, z);
+                p[16 * ch + i / 2] = pack_f16(z.x, z.y);
+            }
+            add = __fmaf_rn(sum.x + sum.y, q.z, add);
+        }
+    }
+}
+
+template <typename TQ, int D>
+__global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
+    using S = Shape<D>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::OFF_BAR);
+    uint64_t *qfull = bars, *kfull = bars + 2, *kempty = bars + 4, *vfull = bars + 6, *vempty = bars + 8, *sfull = bars + 10,
+             *pfull = bars + 12, *ofull = bars + 14, *drain = bars + 16;
+    __shared__ uint32_t tmem_base_sm;
+    __shared__ int abort_sm;
+    volatile int *abort_flag = &abort_sm;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+
+    if (threadIdx.x == 0) {
+        abort_sm = 0;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(qfull + i, 128);
+            mbar_init(kfull + i, 128);
+            mbar_init(kempty + i, 1);
+            mbar_init(vfull + i, 128);
+            mbar_init(vempty + i, 1);
+            mbar_init(sfull + i, 1);
+            mbar_init(pfull + i, 128);
+            mbar_init(ofull + i, 1);
+        }
+        mbar_init(drain, 1);
+        fence_mbar_init();
+    }
+    if (warp == MMA_WARP) {
+        tmem_alloc_1(&tmem_base_sm, 512);
+        tmem_relinquish_1();
+    }
+    griddep_launch_dependents();
+    griddep_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_sm;    // S0 at 0, S1 at 128, O0 at 256, O1 at 384
+    const Item w = item_of(A, blockIdx.x);
+
+    if (w.any) {
+        const int tiles = w.rows - w.row0 > 128 ? 2 : 1;           // tiles of rows that have any
+        if (warp < SOFT_WARPS) {
+            const int t = warp >> 2, tid = threadIdx.x & 127;
+            const int r = 128 * t + tid, row = w.row0 + r;
+            const bool mine = row < w.rows;
+            const int tok = mine ? row / A.group : w.s.n - 1, hq = w.head * A.group + row % A.group;
+            if (t < tiles) {
+                const uint32_t lane_base = (uint32_t)(warp & 3) << 21;     // 32 lanes a warp, lane in bits 16 on
+                const uint32_t s_tmem = tmem + lane_base + 128 * t, o_tmem = tmem + lane_base + 256 + 128 * t;
+                float rowf = A.scale_log2;
+                // the row of Q: fp16 into the swizzled tile; bf16 lifted to fp16's upper range by a power of two
+                {
+                    uint4 v[D / 8];
+                    const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const TQ *>(A.q.data) +
+                                                                       (int64_t)(w.s.row0 + tok) * A.q.ld_tok +
+                                                                       (int64_t)hq * A.q.ld_head);
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) v[i] = mine ? src[i] : make_uint4(0, 0, 0, 0);
+                    if (!std::is_same<TQ, __half>::value) {
+                        uint32_t top = 0;
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) top = max(top, max(x[k] & 0x7fffu, (x[k] >> 16) & 0x7fffu));
+                        }
+                        const int e = min(max((int)(top >> 7) - 127, -100), 126);
+                        const float f = pow2(14 - e);
+                        rowf *= pow2(e - 14);
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i) {
+                            uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[k] = pack_f16(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
+                            v[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                    }
+                    const uint32_t dst = smem_u32(sm + S::OFF_Q + t * S::OPERAND);
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) st_shared_v4(dst + (i / 8) * (TILE * 128) + sw128_offset(tid, i % 8), v[i]);
+                    fence_proxy_async_smem();
+                    mbar_arrive(qfull + t);
+                }
+                const int64_t at = w.s.start + tok;
+                const int row_hi = min(clamp_pos(at + 1), w.hi), row_lo = A.window ? clamp_pos(at + 1 - A.window) : 0;
+                float base = 0.0f, l = 0.0f;
+                bool has = false, settled = false, ok = true;
+                for (int it = 0; it < w.nt && ok; ++it) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(sfull + t, it & 1, abort_flag, A.timeout_ns));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const int key0 = (w.t0 + it) * TILE, slot = it % SLOTS;
+                    const bool whole = whole_tile(w, key0);
+                    const float4 *sc = reinterpret_cast<const float4 *>(sm + S::OFF_SC) + slot * 8;
+                    uint32_t p[TILE / 2];
+                    float add, top;
+                    for (int pass = 0;; ++pass) {
+                        if (whole) soft_tile<false>(s_tmem, sc, rowf, base, 0, 0, p, add, top);
+                        else soft_tile<true>(s_tmem, sc, rowf, base, row_lo - key0, row_hi - key0, p, add, top);
+                        if (pass || (settled && !__any_sync(0xffffffffu, top > kLift + kSlack))) break;
+                        // seldom: raise the references, and take the tile again
+                        float up = 0.0f, f = 1.0f;
+                        if (has) {
+                            up = fmaxf(top - kLift, 0.0f);
+                            f = ex2(-up);
+                        } else if (top > -INFINITY) {
+                            up = top - kLift;              // the row's first keys: its sums are still 0
+                            has = true;
+                        }
+                        base += up;
+                        l *= f;
+                        if (it > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+#pragma unroll
+                            for (int ch = 0; ch < D / 32; ++ch) {
+                                float o[32];
+                                uint32_t b[32];
+                                tmem_ld_32x32b_x32_sync(o_tmem + 32 * ch, o);
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) b[k] = __float_as_uint(o[k] * f);
+                                tmem_st_32x32b_x32(o_tmem + 32 * ch, b);
+                            }
+                        }
+                        settled = __all_sync(0xffffffffu, has);
+                    }
+                    l += add;
+                    if (!whole) {                          // NaN values were taken out of the product: into the sums of who sees them
+                        const uint32_t *bad = reinterpret_cast<const uint32_t *>(sm + S::OFF_NAN + slot * TILE);
+                        for (int k = 0; k < TILE / 4; ++k) {
+                            const uint32_t x = bad[k];
+                            if (!x) continue;
+                            for (int n = 0; n < 4; ++n) {
+                                const int key = key0 + 4 * k + n;
+                                if (((x >> (8 * n)) & 1) && key >= row_lo && key < row_hi) l = NAN;
+                            }
+                        }
+                    }
+                    {
+                        uint32_t b[32];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) b[k] = p[32 * h + k];
+                            tmem_st_32x32b_x32(s_tmem + 32 * h, b);
+                        }
+                    }
+                    tmem_wait_st();
+                    tc_fence_before();
+                    mbar_arrive(pfull + t);
+                }
+                if (ok && w.nt > 0) {
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(ofull + t, 0, abort_flag, A.timeout_ns));
+                    tc_fence_after();
+                }
+                if (ok) {
+                    const float m = has ? base : -INFINITY;
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    TQ *dst = static_cast<TQ *>(const_cast<void *>(A.out.data)) + (int64_t)(w.s.row0 + tok) * A.out.ld_tok +
+                              (int64_t)hq * A.out.ld_head;
+                    const int64_t slot = (int64_t)blockIdx.x * ROWS + r;
+#pragma unroll
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        float o[32];
+                        if (w.nt > 0) {
+                            tmem_ld_32x32b_x32_sync(o_tmem + 32 * ch, o);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = 0.0f;
+                        }
+                        if (mine) {
+#pragma unroll
+                            for (int k = 0; k < 32; k += 8) {
+                                float x[8];
+#pragma unroll
+                                for (int n = 0; n < 8; ++n) x[n] = A.splits == 1 ? o[k + n] * inv : o[k + n];
+                                if (A.splits == 1) store_n(dst + 32 * ch + k, x);
+                                else store_n(A.part_o + slot * D + 32 * ch + k, x);
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (mine) {
+                        if (A.splits > 1) {
+                            A.part_ml[2 * slot] = m;
+                            A.part_ml[2 * slot + 1] = l;
+                        } else if (A.lse) {
+                            A.lse[(int64_t)(w.s.row0 + tok) * A.q.heads + hq] =
+                                l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+                        }
+                    }
+                }
+            }
+        } else if (warp < MMA_WARP) {
+            // ---- codes to operands: values of a tile, then its keys and scales (so that everything a tile's
+            // softmax reads is there before its scores are)
+            constexpr int PER = D / 16;                            // 16-byte chunks of codes a row, and loads a thread
+            constexpr int STEP = 128 / PER;                        // rows between a thread's loads
+            const int t = threadIdx.x - 32 * CONV_WARP, chunk = t % PER, r0 = t / PER;
+            const int page_bits = 31 - __clz(A.C.page);
+            if (t == 0 && w.s.len > (A.B.max_pages * A.C.page < kMaxLen ? A.B.max_pages * A.C.page : kMaxLen))
+                atomicOr(&g_dev_error, kDevErrBadIndex);
+            // first row of block `lane` (of 8) of a tile in the pool; -1: no such keys, or a bad page
+            auto block_rows = [&](int it) -> int {
+                const int pos = (w.t0 + it) * TILE + 16 * lane;
+                if (lane >= 8 || it >= w.nt || pos >= w.hi) return -1;
+                const int64_t page = A.B.pages[(int64_t)w.b * A.B.ld_pages + (pos >> page_bits)];
+                if (page < 0 || page >= A.C.n_pages) {
+                    atomicOr(&g_dev_error, kDevErrBadIndex);
+                    return -1;
+                }
+                return (int)((page * A.C.heads + w.head) * A.C.page) + (pos & (A.C.page - 1));
+            };
+            auto load = [&](const uint8_t *codes, int rows, uint4 (&v)[PER]) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int row = r0 + STEP * i;
+                    const int first = __shfl_sync(0xffffffffu, rows, row / 16);
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (first >= 0)
+                        v[i] = *reinterpret_cast<const uint4 *>(codes + (int64_t)(first + row % 16) * D + 16 * chunk);
+                }
+            };
+            // lanes 0-7 the key scale of a block, 8-15 its value scale; -1 where there is none
+            auto load_scale = [&](int rows) {
+                const int first = __shfl_sync(0xffffffffu, rows, lane & 7);
+                return lane < 16 && first >= 0 ? A.C.scales[lane >> 3][first / 16] : -1.0f;
+            };
+            auto store = [&](uint8_t *dst, const uint4 (&v)[PER]) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    const int row = r0 + STEP * i;
+                    // 16 codes: chunks 2 c and 2 c + 1 of the row's half; lanes of the other half store theirs in
+                    // the other order, so that eight lanes always touch eight different bank groups
+                    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    const uint4 lo = make_uint4(cvt_lo(x[0]), cvt_hi(x[0]), cvt_lo(x[1]), cvt_hi(x[1]));
+                    const uint4 hi = make_uint4(cvt_lo(x[2]), cvt_hi(x[2]), cvt_lo(x[3]), cvt_hi(x[3]));
+                    const uint32_t half = smem_u32(dst) + (chunk / 4) * (TILE * 128), c = 2 * (chunk % 4);
+                    const bool swap = (chunk / 4) & 1;
+                    st_shared_v4(half + sw128_offset(row, c + swap), swap ? hi : lo);
+                    st_shared_v4(half + sw128_offset(row, c + 1 - swap), swap ? lo : hi);
+                }
+            };
+            bool ok = true;
+            uint4 kc[PER], vc[PER];
+            int rows = block_rows(0);
+            load(A.C.codes[1], rows, vc);
+            load(A.C.codes[0], rows, kc);
+            float scale = load_scale(rows);
+            rows = block_rows(1);
+            for (int it = 0; it < w.nt && ok; ++it) {
+                const int st = it & 1, key0 = (w.t0 + it) * TILE, slot = it % SLOTS;
+                const uint32_t ph = ((it >> 1) & 1) ^ 1;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(vempty + st, ph, abort_flag, A.timeout_ns));
+                if (!ok) break;
+                if (!whole_tile(w, key0)) {
+#pragma unroll
+                    for (int i = 0; i < PER; ++i) {
+                        const int row = r0 + STEP * i;
+                        uint32_t x[4] = {vc[i].x, vc[i].y, vc[i].z, vc[i].w}, any = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (key0 + row >= w.hi) x[k] = 0;
+                            const uint32_t nan = nan_bytes(x[k]);
+                            any |= nan;
+                            x[k] &= ~((nan >> 7) * 0xffu);
+                        }
+                        vc[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        const uint32_t votes = __ballot_sync(0xffffffffu, any != 0);
+                        if (chunk == 0)
+                            sm[S::OFF_NAN + slot * TILE + row] = (votes >> (lane & ~(PER - 1))) & ((1u << PER) - 1) ? 1 : 0;
+                    }
+                }
+                store(sm + S::OFF_V + st * S::OPERAND, vc);
+                fence_proxy_async_smem();
+                mbar_arrive(vfull + st);
+                load(A.C.codes[1], rows, vc);
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(kempty + st, ph, abort_flag, A.timeout_ns));
+                if (!ok) break;
+                if (warp == CONV_WARP) {
+                    const float vs = __shfl_sync(0xffffffffu, scale, (lane & 7) + 8);
+                    if (lane < 8) {
+                        const uint32_t bits = __float_as_uint(vs);
+                        float4 q = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
+                        if (scale >= 0.0f && vs >= 0.0f)
+                            q = make_float4(scale, (float)((int)(bits >> 23) - 127), __uint_as_float(0x7f000000u - bits), 0.0f);
+                        reinterpret_cast<float4 *>(sm + S::OFF_SC)[slot * 8 + lane] = q;
+                    }
+                }
+                store(sm + S::OFF_K + st * S::OPERAND, kc);
+                fence_proxy_async_smem();
+                mbar_arrive(kfull + st);
+                load(A.C.codes[0], rows, kc);
+                scale = load_scale(rows);
+                rows = block_rows(it + 2);
+            }
+        } else if (lane == 0 && w.nt > 0) {
+            // ---- the products
+            constexpr uint32_t QK = mma_idesc_f16_f32(128, TILE), PV = mma_idesc_f16_f32(128, D) | (1u << 16);   // V: rows along D
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t ph) {
+                ok = ok && mbar_wait_bounded(bar, ph, abort_flag, A.timeout_ns);
+            };
+            auto scores = [&](int t, int st) {
+                const uint64_t a = sw128_kmajor_desc(smem_u32(sm + S::OFF_Q + t * S::OPERAND));
+                const uint64_t b = sw128_kmajor_desc(smem_u32(sm + S::OFF_K + st * S::OPERAND));
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    const uint64_t off = (uint64_t)(((k / 4) * TILE * 128 + (k % 4) * 32) >> 4);
+                    mma_f16_ss_1(tmem + 128 * t, a + off, b + off, QK, k > 0);
+                }
+                mma_commit_1(sfull + t);
+            };
+            for (int t = 0; t < tiles; ++t) {
+                wait(qfull + t, 0);
+                if (t == 0) wait(kfull, 0);
+                if (!ok) break;
+                tc_fence_after();
+                scores(t, 0);
+            }
+            if (ok) mma_commit_1(kempty);
+            for (int it = 0; it < w.nt && ok; ++it) {
+                const int st = it & 1;
+                wait(vfull + st, (it >> 1) & 1);
+                for (int t = 0; t < tiles && ok; ++t) {
+                    wait(pfull + t, it & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t b = sw128_mnmajor_desc(smem_u32(sm + S::OFF_V + st * S::OPERAND), TILE * 128);
+#pragma unroll
+                    for (int k = 0; k < TILE / 16; ++k)
+                        mma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, b + (uint64_t)((k * 2048) >> 4), PV, it > 0 || k > 0);
+                    if (t == tiles - 1) mma_commit_1(vempty + st);
+                    if (it + 1 < w.nt) {
+                        if (t == 0) wait(kfull + (st ^ 1), ((it + 1) >> 1) & 1);
+                        if (!ok) break;
+                        tc_fence_after();
+                        scores(t, st ^ 1);
+                        if (t == tiles - 1) mma_commit_1(kempty + (st ^ 1));
+                    } else {
+                        mma_commit_1(ofull + t);
+                    }
+                }
+            }
+            mma_commit_1(drain);                                   // every product this thread issued has finished when this fires
+            mbar_wait_bounded(drain, 0, abort_flag, A.timeout_ns);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == MMA_WARP) {
+        tc_fence_after();
+        tmem_dealloc_1(tmem, 512);
+    }
+}
+
+// One warp per (row, query head): the parts of its splits, summed in order.
+template <typename TQ, int D>
+__global__ void __launch_bounds__(256) kv_prefill_join_kernel(const Args A) {
+    constexpr int N = D / 32;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31;
+    const int64_t i = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+    const int64_t t = i / A.q.heads;
+    const int hq = (int)(i % A.q.heads);
+    if (t >= A.T) return;
+    const int b = seq_of_row(A.B, t);
+    if (b < 0) return;
+    const Seq s = seq_info(A.B, b, A.T, A.max_tokens);
+    if (t - s.row0 >= s.n) return;
+    const int row = (int)(t - s.row0) * A.group + hq % A.group;
+    const int tiles = (s.n * A.group + ROWS - 1) / ROWS;
+    const int64_t from_end = tiles - 1 - row / ROWS;
+    const int64_t block0 = ((from_end * A.B.n_seqs + b) * A.C.heads + hq / A.group) * A.splits;
+    const int r = row % ROWS;
+    float mx = -INFINITY;
+    for (int k = 0; k < A.splits; ++k) mx = fmaxf(mx, A.part_ml[((block0 + k) * ROWS + r) * 2]);
+    float L = 0.0f, v[N] = {};
+#pragma unroll 4
+    for (int k = 0; k < A.splits; ++k) {
+        const int64_t at = (block0 + k) * ROWS + r;
+        const float2 p = *reinterpret_cast<const float2 *>(A.part_ml + at * 2);
+        float x[N];
+        load_n(A.part_o + at * D + lane * N, x);
+        if (p.x == -INFINITY) continue;
+        const float f = ex2(p.x - mx);
+        L = __fmaf_rn(f, p.y, L);
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = __fmaf_rn(f, x[n], v[n]);
+    }
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] *= inv;
+    store_n(static_cast<TQ *>(const_cast<void *>(A.out.data)) + t * A.out.ld_tok + (int64_t)hq * A.out.ld_head + lane * N, v);
+    if (A.lse && lane == 0) A.lse[t * A.q.heads + hq] = L == 0.0f ? -INFINITY : (mx + log2f(L)) * 0.6931471805599453f;
+}
+
+}  // namespace pre
+}  // namespace kv
+}  // namespace awq
