@@ -12,7 +12,7 @@
 //   warps 8-11       codes to fp16 operands: 16 codes a load, one tile ahead in
 //                    registers, exact conversion, 128-byte-swizzled tiles in shared
 //                    memory.  One conversion serves 256 rows.
-//   warp 12          one thread issues the products: S = Q K^T from shared memory,
+//   warps 12, 13     issue the products of tile 0, tile 1: S = Q K^T from shared memory,
 //                    O += P' V with P' from tensor memory and V [key][D] as it lies in
 //                    the cache (the operand whose rows run along D).
 //
@@ -44,7 +44,9 @@ using dec::pack_f16;
 
 constexpr int ROWS = 256, TILE = 128;      // query rows and keys per step of a block of threads
 constexpr int SOFT_WARPS = 8, CONV_WARP = 8, MMA_WARP = 12;
-constexpr int THREADS = 32 * 13;
+constexpr int THREADS = 32 * 16;          // warps 14, 15 only give their registers away
+constexpr int SOFT_REGS = 176, CONV_REGS = 104, MMA_REGS = 56;     // of 128 a thread at launch
+static_assert(2 * SOFT_REGS + CONV_REGS + MMA_REGS == 4 * 128, "the block's registers");
 constexpr int SLOTS = 4;                   // tiles whose scales are kept
 
 template <int D> struct Shape {
@@ -53,7 +55,8 @@ template <int D> struct Shape {
     static constexpr int OFF_SC = 6 * OPERAND;             // float4 [SLOTS][8]: key scale, e, 2^-e of a block's values
     static constexpr int OFF_NAN = OFF_SC + SLOTS * 8 * 16;        // byte [SLOTS][TILE]: the key's values hold a NaN
     static constexpr int OFF_BAR = OFF_NAN + SLOTS * TILE;
-    static constexpr int BYTES = OFF_BAR + 256 + 1024;     // + alignment
+    static constexpr int OFF_ROWS = OFF_BAR + 256;         // int [4][8]: first rows of a tile's blocks in the pool, per warp
+    static constexpr int BYTES = OFF_ROWS + 128 + 1024;    // + alignment
 };
 
 struct Args {
@@ -118,53 +121,130 @@ __device__ __forceinline__ Item item_of(const Args &A, int64_t i) {
 }
 __device__ __forceinline__ bool whole_tile(const Item &w, int key0) { return key0 >= w.all_lo && key0 + TILE <= w.all_hi; }
 
-// Descriptor of an operand whose 16-bit elements run along its M or N rows ([k][64] tiles of
-// 128-byte rows, swizzled): 8 k 1024 bytes apart, the next 64 elements `leading` bytes on.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t leading) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(leading >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
+// Upper words of the operand descriptors (the lower word is address / 16 | leading offset / 16 << 16): 128-byte
+// swizzle, eight rows 1024 bytes apart.  V's elements run along its rows ([key][64] tiles of 128-byte rows):
+// eight keys 1024 bytes apart, the next 64 elements of D the leading offset on.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kDescK = 1u << 16, kDescV = (uint32_t)((TILE * 128) >> 4) << 16;
+template <uint32_t LOW>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a | LOW), "r"(b | LOW), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescHigh)
+        : "memory");
+}
+template <uint32_t LOW>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b | LOW), "r"(idesc), "r"((uint32_t)accumulate), "n"(kDescHigh)
+        : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
-// One tile's scores of one row, all 128: P' packed, block sums into `add` (scaled by 2^-e), the largest
-// z = x + e - base.  MASKED: keys outside [lo, hi) of the tile are hidden.
+// 64 columns of a warp's 32 lanes, on their way (tmem_arrive makes them usable) -- the registers are not to be
+// touched before it.
+__device__ __forceinline__ void tmem_issue_64(uint32_t taddr, uint32_t (&r)[64]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, "
+        "%22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32, %33, %34, %35, %36, %37, %38, %39, %40, %41, "
+        "%42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, "
+        "%62, %63}, [%64];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+          "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+          "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]),
+          "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]),
+          "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]),
+          "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]),
+          "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_arrive(uint32_t (&r)[64]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                   "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                   "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                   "+r"(r[29]), "+r"(r[30]), "+r"(r[31]), "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]),
+                   "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]), "+r"(r[40]), "+r"(r[41]), "+r"(r[42]),
+                   "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]), "+r"(r[48]), "+r"(r[49]),
+                   "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]), "+r"(r[56]),
+                   "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+                 :
+                 : "memory");
+}
+
+// Half a tile's scores of one row, 64: P' packed, block sums into `add` (scaled by 2^-e), the largest
+// z = x + e - base.  MASKED: keys outside [lo, hi) of the half are hidden.
 template <bool MASKED>
-__device__ __forceinline__ void soft_tile(uint32_t s_tmem, const float4 *sc, float rowf, float base, int lo, int hi,
+__device__ __forceinline__ void soft_half(const uint32_t (&v)[64], const float4 (&sc)[4], float rowf, float base, int lo, int hi,
+                                          uint32_t *p, float &add, float &top) {
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        const float4 q = sc[b];
+        const float2 f = make_float2(rowf * q.x, rowf * q.x), c = make_float2(q.y - base, q.y - base);
+        float2 sum = make_float2(0.0f, 0.0f);
+        float big = -INFINITY;
+#pragma unroll
+        for (int k = 0; k < 16; k += 2) {
+            const int i = 16 * b + k;
+            float2 z = fma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), f, c);
+            if (MASKED) {
+                if (i < lo || i >= hi) z.x = -INFINITY;
+                if (i + 1 < lo || i + 1 >= hi) z.y = -INFINITY;
+            }
+            big = fmax3(big, z.x, z.y);
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            sum = __fadd2_rn(sum, z);
+            p[i / 2] = pack_f16(z.x, z.y);
+        }
+        add = __fmaf_rn(sum.x + sum.y, q.z, add);
+        top = fmaxf(top, big);
+    }
+}
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+// A whole tile: the second half's scores come out of tensor memory while the first half's are worked on.
+// The scales are fetched ahead too: while the tensor core reads its operands from shared memory a load
+// from there takes several times as long (together 450 clocks a tile where each was fetched for its block).
+template <bool MASKED>
+__device__ __forceinline__ void soft_tile(uint32_t s_tmem, uint32_t sc, float rowf, float base, int lo, int hi,
                                           uint32_t (&p)[TILE / 2], float &add, float &top) {
     add = 0.0f;
     top = -INFINITY;
+    uint32_t v0[64], v1[64];
+    float4 q[4];
+    tmem_issue_64(s_tmem, v0);
 #pragma unroll
-    for (int ch = 0; ch < 4; ++ch) {
-        float v[32];
-        tmem_ld_32x32b_x32_sync(s_tmem + 32 * ch, v);
+    for (int b = 0; b < 4; ++b) q[b] = lds_f4(sc + 16 * b);
+    tmem_arrive(v0);
+    tmem_issue_64(s_tmem + 64, v1);
+    float4 q1[4];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-            const float4 q = sc[2 * ch + b];
-            const float2 f = make_float2(rowf * q.x, rowf * q.x), c = make_float2(q.y - base, q.y - base);
-            float2 sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-                const int i = 16 * b + k;
-                float2 z = fma2_rn(make_float2(v[i], v[i + 1]), f, c);
-                if (MASKED) {
-                    const int key = 32 * ch + i;
-                    if (key < lo || key >= hi) z.x = -INFINITY;
-                    if (key + 1 < lo || key + 1 >= hi) z.y = -INFINITY;
-                }
-                top = fmax3(top, z.x, z.y);
-                z.x = ex2(z.x);
-                z.y = ex2(z.y);
-                sum = __fadd2_rn(sum, z);
-                p[16 * ch + i / 2] = pack_f16(z.x, z.y);
-            }
-            add = __fmaf_rn(sum.x + sum.y, q.z, add);
-        }
-    }
+    for (int b = 0; b < 4; ++b) q1[b] = lds_f4(sc + 64 + 16 * b);
+    soft_half<MASKED>(v0, q, rowf, base, lo, hi, p, add, top);
+    tmem_arrive(v1);
+    soft_half<MASKED>(v1, q1, rowf, base, lo - 64, hi - 64, p + 32, add, top);
 }
+
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <typename TQ, int D>
 __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
@@ -184,14 +264,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(qfull + i, 128);
             mbar_init(kfull + i, 128);
-            mbar_init(kempty + i, 1);
+            mbar_init(kempty + i, 2);
             mbar_init(vfull + i, 128);
-            mbar_init(vempty + i, 1);
+            mbar_init(vempty + i, 2);
             mbar_init(sfull + i, 1);
             mbar_init(pfull + i, 128);
             mbar_init(ofull + i, 1);
+            mbar_init(drain + i, 1);
         }
-        mbar_init(drain, 1);
         fence_mbar_init();
     }
     if (warp == MMA_WARP) {
@@ -209,6 +289,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
     if (w.any) {
         const int tiles = w.rows - w.row0 > 128 ? 2 : 1;           // tiles of rows that have any
         if (warp < SOFT_WARPS) {
+            regs_up<SOFT_REGS>();
             const int t = warp >> 2, tid = threadIdx.x & 127;
             const int r = 128 * t + tid, row = w.row0 + r;
             const bool mine = row < w.rows;
@@ -261,7 +342,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                     tc_fence_after();
                     const int key0 = (w.t0 + it) * TILE, slot = it % SLOTS;
                     const bool whole = whole_tile(w, key0);
-                    const float4 *sc = reinterpret_cast<const float4 *>(sm + S::OFF_SC) + slot * 8;
+                    const uint32_t sc = smem_u32(sm + S::OFF_SC) + slot * 128;
                     uint32_t p[TILE / 2];
                     float add, top;
                     for (int pass = 0;; ++pass) {
@@ -360,6 +441,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                 }
             }
         } else if (warp < MMA_WARP) {
+            regs_down<CONV_REGS>();
             // ---- codes to operands: values of a tile, then its keys and scales (so that everything a tile's
             // softmax reads is there before its scores are)
             constexpr int PER = D / 16;                            // 16-byte chunks of codes a row, and loads a thread
@@ -379,14 +461,23 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                 }
                 return (int)((page * A.C.heads + w.head) * A.C.page) + (pos & (A.C.page - 1));
             };
-            auto load = [&](const uint8_t *codes, int rows, uint4 (&v)[PER]) {
+            // this thread's rows of a tile: block first rows through shared memory, then one load each
+            int *mine8 = reinterpret_cast<int *>(sm + S::OFF_ROWS) + 8 * (warp - CONV_WARP);
+            auto rows_of = [&](int rows, int (&at)[PER]) {
+                __syncwarp();
+                if (lane < 8) mine8[lane] = rows;
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int row = r0 + STEP * i;
-                    const int first = __shfl_sync(0xffffffffu, rows, row / 16);
+                    const int row = r0 + STEP * i, first = mine8[row / 16];
+                    at[i] = first < 0 ? -1 : first + row % 16;
+                }
+            };
+            auto load = [&](const uint8_t *codes, const int (&at)[PER], uint4 (&v)[PER]) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
                     v[i] = make_uint4(0, 0, 0, 0);
-                    if (first >= 0)
-                        v[i] = *reinterpret_cast<const uint4 *>(codes + (int64_t)(first + row % 16) * D + 16 * chunk);
+                    if (at[i] >= 0) v[i] = ldg_stream_v4(codes + (int64_t)at[i] * D + 16 * chunk);
                 }
             };
             // lanes 0-7 the key scale of a block, 8-15 its value scale; -1 where there is none
@@ -412,8 +503,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
             bool ok = true;
             uint4 kc[PER], vc[PER];
             int rows = block_rows(0);
-            load(A.C.codes[1], rows, vc);
-            load(A.C.codes[0], rows, kc);
+            int at[PER];
+            rows_of(rows, at);
+            load(A.C.codes[1], at, vc);
+            load(A.C.codes[0], at, kc);
             float scale = load_scale(rows);
             rows = block_rows(1);
             for (int it = 0; it < w.nt && ok; ++it) {
@@ -442,7 +535,8 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                 store(sm + S::OFF_V + st * S::OPERAND, vc);
                 fence_proxy_async_smem();
                 mbar_arrive(vfull + st);
-                load(A.C.codes[1], rows, vc);
+                rows_of(rows, at);
+                load(A.C.codes[1], at, vc);
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(kempty + st, ph, abort_flag, A.timeout_ns));
                 if (!ok) break;
                 if (warp == CONV_WARP) {
@@ -458,60 +552,70 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                 store(sm + S::OFF_K + st * S::OPERAND, kc);
                 fence_proxy_async_smem();
                 mbar_arrive(kfull + st);
-                load(A.C.codes[0], rows, kc);
+                load(A.C.codes[0], at, kc);
                 scale = load_scale(rows);
                 rows = block_rows(it + 2);
             }
-        } else if (lane == 0 && w.nt > 0) {
-            // ---- the products
+        } else if (regs_down<MMA_REGS>(); warp < MMA_WARP + tiles && w.nt > 0) {
+            // ---- the products of one tile: its O += P' V, then its next scores.  The whole warp runs along and one
+            // lane issues, so that addresses stay warp-uniform; with one warp for both tiles, issuing from a
+            // single-lane branch, an instruction took 190 clocks to leave (64 is what it computes).
             constexpr uint32_t QK = mma_idesc_f16_f32(128, TILE), PV = mma_idesc_f16_f32(128, D) | (1u << 16);   // V: rows along D
+            const int t = warp - MMA_WARP;
+            const bool leader = elect_one();
+            const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0) >> 4, tm = __shfl_sync(0xffffffffu, tmem, 0);
+            const uint32_t q_lo = base + ((S::OFF_Q + t * S::OPERAND) >> 4), k_lo = base + (S::OFF_K >> 4), v_lo = base + (S::OFF_V >> 4);
+            const uint32_t s_tmem = tm + 128 * t, o_tmem = tm + 256 + 128 * t;
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t ph) {
-                ok = ok && mbar_wait_bounded(bar, ph, abort_flag, A.timeout_ns);
+                ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, ph, abort_flag, A.timeout_ns));
             };
-            auto scores = [&](int t, int st) {
-                const uint64_t a = sw128_kmajor_desc(smem_u32(sm + S::OFF_Q + t * S::OPERAND));
-                const uint64_t b = sw128_kmajor_desc(smem_u32(sm + S::OFF_K + st * S::OPERAND));
+            auto scores = [&](int st) {
+                if (leader) {
+                    const uint32_t b = k_lo + st * (S::OPERAND >> 4);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    const uint64_t off = (uint64_t)(((k / 4) * TILE * 128 + (k % 4) * 32) >> 4);
-                    mma_f16_ss_1(tmem + 128 * t, a + off, b + off, QK, k > 0);
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint32_t off = ((k / 4) * TILE * 128 + (k % 4) * 32) >> 4;
+                        mma_ss<kDescK>(s_tmem, q_lo + off, b + off, QK, k > 0);
+                    }
+                    mma_commit_1(sfull + t);
+                    mma_commit_1(kempty + st);
+                    if (tiles == 1) mma_commit_1(kempty + st);     // for the tile that is not there
                 }
-                mma_commit_1(sfull + t);
+                __syncwarp();
             };
-            for (int t = 0; t < tiles; ++t) {
-                wait(qfull + t, 0);
-                if (t == 0) wait(kfull, 0);
-                if (!ok) break;
+            wait(qfull + t, 0);
+            wait(kfull, 0);
+            if (ok) {
                 tc_fence_after();
-                scores(t, 0);
+                scores(0);
             }
-            if (ok) mma_commit_1(kempty);
             for (int it = 0; it < w.nt && ok; ++it) {
                 const int st = it & 1;
                 wait(vfull + st, (it >> 1) & 1);
-                for (int t = 0; t < tiles && ok; ++t) {
-                    wait(pfull + t, it & 1);
+                wait(pfull + t, it & 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (leader) {
+                    const uint32_t b = v_lo + st * (S::OPERAND >> 4);
+                    mma_ts<kDescV>(o_tmem, s_tmem, b, PV, it > 0);
+#pragma unroll
+                    for (int k = 1; k < TILE / 16; ++k) mma_ts<kDescV>(o_tmem, s_tmem + 8 * k, b + ((k * 2048) >> 4), PV, true);
+                    mma_commit_1(vempty + st);
+                    if (tiles == 1) mma_commit_1(vempty + st);
+                    if (it + 1 == w.nt) mma_commit_1(ofull + t);
+                }
+                __syncwarp();
+                if (it + 1 < w.nt) {
+                    wait(kfull + (st ^ 1), ((it + 1) >> 1) & 1);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t b = sw128_mnmajor_desc(smem_u32(sm + S::OFF_V + st * S::OPERAND), TILE * 128);
-#pragma unroll
-                    for (int k = 0; k < TILE / 16; ++k)
-                        mma_f16_ts(tmem + 256 + 128 * t, tmem + 128 * t + 8 * k, b + (uint64_t)((k * 2048) >> 4), PV, it > 0 || k > 0);
-                    if (t == tiles - 1) mma_commit_1(vempty + st);
-                    if (it + 1 < w.nt) {
-                        if (t == 0) wait(kfull + (st ^ 1), ((it + 1) >> 1) & 1);
-                        if (!ok) break;
-                        tc_fence_after();
-                        scores(t, st ^ 1);
-                        if (t == tiles - 1) mma_commit_1(kempty + (st ^ 1));
-                    } else {
-                        mma_commit_1(ofull + t);
-                    }
+                    scores(st ^ 1);
                 }
             }
-            mma_commit_1(drain);                                   // every product this thread issued has finished when this fires
-            mbar_wait_bounded(drain, 0, abort_flag, A.timeout_ns);
+            if (leader) mma_commit_1(drain + t);                   // every product this thread issued has finished when this fires
+            __syncwarp();
+            mbar_wait_bounded(drain + t, 0, abort_flag, A.timeout_ns);
         }
     }
     __syncwarp();
