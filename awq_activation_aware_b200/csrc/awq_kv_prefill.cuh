@@ -16,12 +16,14 @@
 //                    O += P' V with P' from tensor memory and V [key][D] as it lies in
 //                    the cache (the operand whose rows run along D).
 //
-// While one tile's softmax runs the tensor core works for the other.  Scales and
+// The scores of a row tile have two buffers of 64 keys: those of the next step are ready
+// when a step's P' is, so the softmax warps never wait for their own products (with one
+// buffer of 128 keys a tile went through softmax, products and back, 4900 clocks a turn
+// of which the softmax was 2100).  Scales and
 // references are those of the kernel for few rows (awq_kv_decode.cuh): the key scale
 // multiplies the score, the value scale is an exponent, a row's reference is raised
 // only when a score passes it by 2^6, and then its part of O is rescaled in tensor
-// memory; O's products of the step before are done by then, since they were issued
-// before the scores whose completion the softmax waited for.
+// memory, after the products of the step before.
 //
 // With too few blocks of rows to fill the machine the keys are split over several
 // blocks of threads, and a second kernel joins their parts in order.
@@ -42,7 +44,8 @@ using dec::kSlack;
 using dec::nan_bytes;
 using dec::pack_f16;
 
-constexpr int ROWS = 256, TILE = 128;      // query rows and keys per step of a block of threads
+constexpr int ROWS = 256, TILE = 128;      // query rows of a block of threads, keys per converted tile
+constexpr int STEP = 64;                   // keys per softmax step
 constexpr int SOFT_WARPS = 8, CONV_WARP = 8, MMA_WARP = 12;
 constexpr int THREADS = 32 * 16;          // warps 14, 15 only give their registers away
 constexpr int SOFT_REGS = 176, CONV_REGS = 104, MMA_REGS = 56;     // of 128 a thread at launch
@@ -79,7 +82,7 @@ struct Item {
     int b, head, split;
     int row0, rows;                        // first row, rows of the sequence and head
     int hi;                                // keys that exist for some row
-    int t0, nt;                            // first tile of keys, and how many (of this split)
+    int t0, nt, ns;                        // first tile of keys, how many (of this split), and their steps
     int all_lo, all_hi;                    // keys that every row sees
     bool any;
 };
@@ -114,6 +117,7 @@ __device__ __forceinline__ Item item_of(const Args &A, int64_t i) {
     w.t0 += j0;
     w.nt = nt - j0 < per ? nt - j0 : per;
     if (w.nt < 0) w.nt = 0;
+    w.ns = 2 * w.nt - (w.nt > 0 && (w.t0 + w.nt) * TILE - STEP >= w.hi ? 1 : 0);   // a last half tile without keys is left out
     w.all_hi = clamp_pos(w.s.start + first + 1);
     if (w.all_hi > w.hi) w.all_hi = w.hi;
     w.all_lo = A.window ? clamp_pos(w.s.start + last + 1 - A.window) : 0;
@@ -186,15 +190,29 @@ __device__ __forceinline__ void tmem_arrive(uint32_t (&r)[64]) {
                  : "memory");
 }
 
-// Half a tile's scores of one row, 64: P' packed, block sums into `add` (scaled by 2^-e), the largest
-// z = x + e - base.  MASKED: keys outside [lo, hi) of the half are hidden.
+__device__ __forceinline__ float4 lds_f4(uint32_t a) {
+    float4 v;
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
+    return v;
+}
+// One step's scores of one row, 64: P' packed, block sums into `add` (scaled by 2^-e), the largest
+// z = x + e - base.  MASKED: keys outside [lo, hi) of the step are hidden.  The scales are fetched while
+// the scores come: when the tensor core reads its operands from shared memory a load from there takes
+// several times as long.
 template <bool MASKED>
-__device__ __forceinline__ void soft_half(const uint32_t (&v)[64], const float4 (&sc)[4], float rowf, float base, int lo, int hi,
-                                          uint32_t *p, float &add, float &top) {
+__device__ __forceinline__ void soft_step(uint32_t s_tmem, uint32_t sc, float rowf, float base, int lo, int hi,
+                                          uint32_t (&p)[STEP / 2], float &add, float &top) {
+    uint32_t v[64];
+    float4 q[4];
+    tmem_issue_64(s_tmem, v);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) q[b] = lds_f4(sc + 16 * b);
+    tmem_arrive(v);
+    add = 0.0f;
+    top = -INFINITY;
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
-        const float4 q = sc[b];
-        const float2 f = make_float2(rowf * q.x, rowf * q.x), c = make_float2(q.y - base, q.y - base);
+        const float2 f = make_float2(rowf * q[b].x, rowf * q[b].x), c = make_float2(q[b].y - base, q[b].y - base);
         float2 sum = make_float2(0.0f, 0.0f);
         float big = -INFINITY;
 #pragma unroll
@@ -211,36 +229,9 @@ __device__ __forceinline__ void soft_half(const uint32_t (&v)[64], const float4 
             sum = __fadd2_rn(sum, z);
             p[i / 2] = pack_f16(z.x, z.y);
         }
-        add = __fmaf_rn(sum.x + sum.y, q.z, add);
+        add = __fmaf_rn(sum.x + sum.y, q[b].z, add);
         top = fmaxf(top, big);
     }
-}
-__device__ __forceinline__ float4 lds_f4(uint32_t a) {
-    float4 v;
-    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(a));
-    return v;
-}
-// A whole tile: the second half's scores come out of tensor memory while the first half's are worked on.
-// The scales are fetched ahead too: while the tensor core reads its operands from shared memory a load
-// from there takes several times as long (together 450 clocks a tile where each was fetched for its block).
-template <bool MASKED>
-__device__ __forceinline__ void soft_tile(uint32_t s_tmem, uint32_t sc, float rowf, float base, int lo, int hi,
-                                          uint32_t (&p)[TILE / 2], float &add, float &top) {
-    add = 0.0f;
-    top = -INFINITY;
-    uint32_t v0[64], v1[64];
-    float4 q[4];
-    tmem_issue_64(s_tmem, v0);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) q[b] = lds_f4(sc + 16 * b);
-    tmem_arrive(v0);
-    tmem_issue_64(s_tmem + 64, v1);
-    float4 q1[4];
-#pragma unroll
-    for (int b = 0; b < 4; ++b) q1[b] = lds_f4(sc + 64 + 16 * b);
-    soft_half<MASKED>(v0, q, rowf, base, lo, hi, p, add, top);
-    tmem_arrive(v1);
-    soft_half<MASKED>(v1, q1, rowf, base, lo - 64, hi - 64, p + 32, add, top);
 }
 
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -253,7 +244,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::OFF_BAR);
     uint64_t *qfull = bars, *kfull = bars + 2, *kempty = bars + 4, *vfull = bars + 6, *vempty = bars + 8, *sfull = bars + 10,
-             *pfull = bars + 12, *ofull = bars + 14, *drain = bars + 16;
+             *pfull = bars + 14, *pvdone = bars + 18, *drain = bars + 20;      // sfull, pfull: [tile][buffer]
     __shared__ uint32_t tmem_base_sm;
     __shared__ int abort_sm;
     volatile int *abort_flag = &abort_sm;
@@ -267,10 +258,12 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
             mbar_init(kempty + i, 2);
             mbar_init(vfull + i, 128);
             mbar_init(vempty + i, 2);
+            mbar_init(pvdone + i, 1);
+            mbar_init(drain + i, 1);
+        }
+        for (int i = 0; i < 4; ++i) {
             mbar_init(sfull + i, 1);
             mbar_init(pfull + i, 128);
-            mbar_init(ofull + i, 1);
-            mbar_init(drain + i, 1);
         }
         fence_mbar_init();
     }
@@ -283,7 +276,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base_sm;    // S0 at 0, S1 at 128, O0 at 256, O1 at 384
+    const uint32_t tmem = tmem_base_sm;    // S of tile t, buffer b: at 128 t + 64 b; O: at 256 + 128 t
     const Item w = item_of(A, blockIdx.x);
 
     if (w.any) {
@@ -336,20 +329,21 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                 const int row_hi = min(clamp_pos(at + 1), w.hi), row_lo = A.window ? clamp_pos(at + 1 - A.window) : 0;
                 float base = 0.0f, l = 0.0f;
                 bool has = false, settled = false, ok = true;
-                for (int it = 0; it < w.nt && ok; ++it) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(sfull + t, it & 1, abort_flag, A.timeout_ns));
+                for (int j = 0; j < w.ns && ok; ++j) {
+                    const int buf = j & 1;
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(sfull + 2 * t + buf, (j >> 1) & 1, abort_flag, A.timeout_ns));
                     if (!ok) break;
                     tc_fence_after();
-                    const int key0 = (w.t0 + it) * TILE, slot = it % SLOTS;
-                    const bool whole = whole_tile(w, key0);
-                    const uint32_t sc = smem_u32(sm + S::OFF_SC) + slot * 128;
-                    uint32_t p[TILE / 2];
+                    const int key0 = w.t0 * TILE + j * STEP, slot = (j >> 1) % SLOTS;
+                    const bool whole = whole_tile(w, key0 - buf * STEP);
+                    const uint32_t sc = smem_u32(sm + S::OFF_SC) + slot * 128 + 64 * buf;
+                    uint32_t p[STEP / 2];
                     float add, top;
                     for (int pass = 0;; ++pass) {
-                        if (whole) soft_tile<false>(s_tmem, sc, rowf, base, 0, 0, p, add, top);
-                        else soft_tile<true>(s_tmem, sc, rowf, base, row_lo - key0, row_hi - key0, p, add, top);
+                        if (whole) soft_step<false>(s_tmem + 64 * buf, sc, rowf, base, 0, 0, p, add, top);
+                        else soft_step<true>(s_tmem + 64 * buf, sc, rowf, base, row_lo - key0, row_hi - key0, p, add, top);
                         if (pass || (settled && !__any_sync(0xffffffffu, top > kLift + kSlack))) break;
-                        // seldom: raise the references, and take the tile again
+                        // seldom: raise the references, and take the step again
                         float up = 0.0f, f = 1.0f;
                         if (has) {
                             up = fmaxf(top - kLift, 0.0f);
@@ -360,7 +354,10 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                         }
                         base += up;
                         l *= f;
-                        if (it > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                        if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
+                            // the step before is the last whose product may still run: this one's P' is not out yet
+                            ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone + t, (j - 1) & 1, abort_flag, A.timeout_ns));
+                            tc_fence_after();
 #pragma unroll
                             for (int ch = 0; ch < D / 32; ++ch) {
                                 float o[32];
@@ -373,10 +370,11 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                         }
                         settled = __all_sync(0xffffffffu, has);
                     }
+                    tmem_st_32x32b_x32(s_tmem + 64 * buf, p);
                     l += add;
                     if (!whole) {                          // NaN values were taken out of the product: into the sums of who sees them
-                        const uint32_t *bad = reinterpret_cast<const uint32_t *>(sm + S::OFF_NAN + slot * TILE);
-                        for (int k = 0; k < TILE / 4; ++k) {
+                        const uint32_t *bad = reinterpret_cast<const uint32_t *>(sm + S::OFF_NAN + slot * TILE + buf * STEP);
+                        for (int k = 0; k < STEP / 4; ++k) {
                             const uint32_t x = bad[k];
                             if (!x) continue;
                             for (int n = 0; n < 4; ++n) {
@@ -385,23 +383,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                             }
                         }
                     }
-                    {
-                        uint32_t b[32];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) b[k] = p[32 * h + k];
-                            tmem_st_32x32b_x32(s_tmem + 32 * h, b);
-                        }
-                    }
                     tmem_wait_st();
                     tc_fence_before();
-                    mbar_arrive(pfull + t);
+                    mbar_arrive(pfull + 2 * t + buf);
                 }
-                if (ok && w.nt > 0) {
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(ofull + t, 0, abort_flag, A.timeout_ns));
-                    tc_fence_after();
-                }
+                // the last two products, in turn: a parity tells phase n only from n + 1, and of the earlier ones the last
+                // scores that arrived say that they are done
+                for (int j = w.ns > 1 ? w.ns - 2 : 0; j < w.ns && ok; ++j)
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone + t, j & 1, abort_flag, A.timeout_ns));
+                tc_fence_after();
                 if (ok) {
                     const float m = has ? base : -INFINITY;
                     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -411,7 +401,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
 #pragma unroll
                     for (int ch = 0; ch < D / 32; ++ch) {
                         float o[32];
-                        if (w.nt > 0) {
+                        if (w.ns > 0) {
                             tmem_ld_32x32b_x32_sync(o_tmem + 32 * ch, o);
                         } else {
 #pragma unroll
@@ -560,7 +550,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
             // ---- the products of one tile: its O += P' V, then its next scores.  The whole warp runs along and one
             // lane issues, so that addresses stay warp-uniform; with one warp for both tiles, issuing from a
             // single-lane branch, an instruction took 190 clocks to leave (64 is what it computes).
-            constexpr uint32_t QK = mma_idesc_f16_f32(128, TILE), PV = mma_idesc_f16_f32(128, D) | (1u << 16);   // V: rows along D
+            constexpr uint32_t QK = mma_idesc_f16_f32(128, STEP), PV = mma_idesc_f16_f32(128, D) | (1u << 16);   // V: rows along D
             const int t = warp - MMA_WARP;
             const bool leader = elect_one();
             const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0) >> 4, tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -570,48 +560,48 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
             auto wait = [&](uint64_t *bar, uint32_t ph) {
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, ph, abort_flag, A.timeout_ns));
             };
-            auto scores = [&](int st) {
+            // what both tiles read is free when both have committed; the tile that is not there is committed for
+            auto release = [&](uint64_t *bar) {
+                mma_commit_1(bar);
+                if (tiles == 1) mma_commit_1(bar);
+            };
+            auto scores = [&](int j) {                             // of step j, into the buffer that P'(j - 2) leaves
+                const int st = (j >> 1) & 1, buf = j & 1;
+                if (buf == 0) wait(kfull + st, (j >> 2) & 1);
+                if (!ok) return;
+                tc_fence_after();
                 if (leader) {
-                    const uint32_t b = k_lo + st * (S::OPERAND >> 4);
+                    const uint32_t b = k_lo + st * (S::OPERAND >> 4) + buf * ((STEP * 128) >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k / 4) * TILE * 128 + (k % 4) * 32) >> 4;
-                        mma_ss<kDescK>(s_tmem, q_lo + off, b + off, QK, k > 0);
+                        mma_ss<kDescK>(s_tmem + 64 * buf, q_lo + off, b + off, QK, k > 0);
                     }
-                    mma_commit_1(sfull + t);
-                    mma_commit_1(kempty + st);
-                    if (tiles == 1) mma_commit_1(kempty + st);     // for the tile that is not there
+                    mma_commit_1(sfull + 2 * t + buf);
+                    if (buf || j + 1 == w.ns) release(kempty + st);
                 }
                 __syncwarp();
             };
             wait(qfull + t, 0);
-            wait(kfull, 0);
-            if (ok) {
-                tc_fence_after();
-                scores(0);
-            }
-            for (int it = 0; it < w.nt && ok; ++it) {
-                const int st = it & 1;
-                wait(vfull + st, (it >> 1) & 1);
-                wait(pfull + t, it & 1);
+            scores(0);
+            if (w.ns > 1) scores(1);
+            for (int j = 0; j < w.ns && ok; ++j) {
+                const int st = (j >> 1) & 1, buf = j & 1;
+                if (buf == 0) wait(vfull + st, (j >> 2) & 1);
+                wait(pfull + 2 * t + buf, (j >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t b = v_lo + st * (S::OPERAND >> 4);
-                    mma_ts<kDescV>(o_tmem, s_tmem, b, PV, it > 0);
+                    const uint32_t b = v_lo + st * (S::OPERAND >> 4) + buf * ((STEP * 128) >> 4);
+                    mma_ts<kDescV>(o_tmem, s_tmem + 64 * buf, b, PV, j > 0);
 #pragma unroll
-                    for (int k = 1; k < TILE / 16; ++k) mma_ts<kDescV>(o_tmem, s_tmem + 8 * k, b + ((k * 2048) >> 4), PV, true);
-                    mma_commit_1(vempty + st);
-                    if (tiles == 1) mma_commit_1(vempty + st);
-                    if (it + 1 == w.nt) mma_commit_1(ofull + t);
+                    for (int k = 1; k < STEP / 16; ++k)
+                        mma_ts<kDescV>(o_tmem, s_tmem + 64 * buf + 8 * k, b + ((k * 2048) >> 4), PV, true);
+                    mma_commit_1(pvdone + t);
+                    if (buf || j + 1 == w.ns) release(vempty + st);
                 }
                 __syncwarp();
-                if (it + 1 < w.nt) {
-                    wait(kfull + (st ^ 1), ((it + 1) >> 1) & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    scores(st ^ 1);
-                }
+                if (j + 2 < w.ns) scores(j + 2);
             }
             if (leader) mma_commit_1(drain + t);                   // every product this thread issued has finished when this fires
             __syncwarp();
