@@ -373,6 +373,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                     tmem_st_32x32b_x32(s_tmem + 64 * buf, p);
                     l += add;
                     if (!whole) {                          // NaN values were taken out of the product: into the sums of who sees them
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(vfull + ((j >> 1) & 1), (j >> 2) & 1, abort_flag, A.timeout_ns));
                         const uint32_t *bad = reinterpret_cast<const uint32_t *>(sm + S::OFF_NAN + slot * TILE + buf * STEP);
                         for (int k = 0; k < STEP / 4; ++k) {
                             const uint32_t x = bad[k];
@@ -432,10 +433,9 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
             }
         } else if (warp < MMA_WARP) {
             regs_down<CONV_REGS>();
-            // ---- codes to operands: values of a tile, then its keys and scales (so that everything a tile's
-            // softmax reads is there before its scores are)
+            // ---- codes to operands: scales and keys of a tile, then its values (keys first: the scores run ahead)
             constexpr int PER = D / 16;                            // 16-byte chunks of codes a row, and loads a thread
-            constexpr int STEP = 128 / PER;                        // rows between a thread's loads
+            constexpr int SKIP = 128 / PER;                            // rows between a thread's loads
             const int t = threadIdx.x - 32 * CONV_WARP, chunk = t % PER, r0 = t / PER;
             const int page_bits = 31 - __clz(A.C.page);
             if (t == 0 && w.s.len > (A.B.max_pages * A.C.page < kMaxLen ? A.B.max_pages * A.C.page : kMaxLen))
@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int row = r0 + STEP * i, first = mine8[row / 16];
+                    const int row = r0 + SKIP * i, first = mine8[row / 16];
                     at[i] = first < 0 ? -1 : first + row % 16;
                 }
             };
@@ -475,10 +475,13 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                 const int first = __shfl_sync(0xffffffffu, rows, lane & 7);
                 return lane < 16 && first >= 0 ? A.C.scales[lane >> 3][first / 16] : -1.0f;
             };
-            auto store = [&](uint8_t *dst, const uint4 (&v)[PER]) {
+            // the conversions stay behind the wait before them: hoisted above it they wait for the loads
+            auto store = [&](uint8_t *dst, uint4 (&v)[PER]) {
+#pragma unroll
+                for (int i = 0; i < PER; ++i) asm volatile("" : "+r"(v[i].x), "+r"(v[i].y), "+r"(v[i].z), "+r"(v[i].w));
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
-                    const int row = r0 + STEP * i;
+                    const int row = r0 + SKIP * i;
                     // 16 codes: chunks 2 c and 2 c + 1 of the row's half; lanes of the other half store theirs in
                     // the other order, so that eight lanes always touch eight different bank groups
                     const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -502,12 +505,31 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
             for (int it = 0; it < w.nt && ok; ++it) {
                 const int st = it & 1, key0 = (w.t0 + it) * TILE, slot = it % SLOTS;
                 const uint32_t ph = ((it >> 1) & 1) ^ 1;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(kempty + st, ph, abort_flag, A.timeout_ns));
+                if (!ok) break;
+                if (warp == CONV_WARP) {
+                    const float vs = __shfl_sync(0xffffffffu, scale, (lane & 7) + 8);
+                    if (lane < 8) {
+                        const uint32_t bits = __float_as_uint(vs);
+                        float4 q = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
+                        if (scale >= 0.0f && vs >= 0.0f)
+                            q = make_float4(scale, (float)((int)(bits >> 23) - 127), __uint_as_float(0x7f000000u - bits), 0.0f);
+                        reinterpret_cast<float4 *>(sm + S::OFF_SC)[slot * 8 + lane] = q;
+                    }
+                }
+                store(sm + S::OFF_K + st * S::OPERAND, kc);
+                fence_proxy_async_smem();
+                mbar_arrive(kfull + st);
+                rows_of(rows, at);
+                load(A.C.codes[0], at, kc);
+                scale = load_scale(rows);
+                rows = block_rows(it + 2);
                 ok = __all_sync(0xffffffffu, mbar_wait_bounded(vempty + st, ph, abort_flag, A.timeout_ns));
                 if (!ok) break;
                 if (!whole_tile(w, key0)) {
 #pragma unroll
                     for (int i = 0; i < PER; ++i) {
-                        const int row = r0 + STEP * i;
+                        const int row = r0 + SKIP * i;
                         uint32_t x[4] = {vc[i].x, vc[i].y, vc[i].z, vc[i].w}, any = 0;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -525,26 +547,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                 store(sm + S::OFF_V + st * S::OPERAND, vc);
                 fence_proxy_async_smem();
                 mbar_arrive(vfull + st);
-                rows_of(rows, at);
                 load(A.C.codes[1], at, vc);
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(kempty + st, ph, abort_flag, A.timeout_ns));
-                if (!ok) break;
-                if (warp == CONV_WARP) {
-                    const float vs = __shfl_sync(0xffffffffu, scale, (lane & 7) + 8);
-                    if (lane < 8) {
-                        const uint32_t bits = __float_as_uint(vs);
-                        float4 q = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
-                        if (scale >= 0.0f && vs >= 0.0f)
-                            q = make_float4(scale, (float)((int)(bits >> 23) - 127), __uint_as_float(0x7f000000u - bits), 0.0f);
-                        reinterpret_cast<float4 *>(sm + S::OFF_SC)[slot * 8 + lane] = q;
-                    }
-                }
-                store(sm + S::OFF_K + st * S::OPERAND, kc);
-                fence_proxy_async_smem();
-                mbar_arrive(kfull + st);
-                load(A.C.codes[0], at, kc);
-                scale = load_scale(rows);
-                rows = block_rows(it + 2);
             }
         } else if (regs_down<MMA_REGS>(); warp < MMA_WARP + tiles && w.nt > 0) {
             // ---- the products of one tile: its O += P' V, then its next scores.  The whole warp runs along and one
