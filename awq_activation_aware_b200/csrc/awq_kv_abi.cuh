@@ -94,8 +94,8 @@ void launch_append(const awq::kv::AppendArgs &A, dim3 grid, cudaStream_t st) {
 }
 
 // Codes as a 2-D tensor of bytes [n_pages * heads * page][D], boxes of `box_rows`
-// rows swizzled over their width.
-bool encode_kv_map(CUtensorMap *m, const void *codes, const awq::kv::Cache &c, int box_rows) {
+// rows, swizzled over their width or as they are.
+bool encode_kv_map(CUtensorMap *m, const void *codes, const awq::kv::Cache &c, int box_rows, bool swizzle = true) {
     EncodeTiledFn fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)c.dim, (cuuint64_t)(c.n_pages * c.heads * c.page)};
@@ -104,7 +104,8 @@ bool encode_kv_map(CUtensorMap *m, const void *codes, const awq::kv::Cache &c, i
     cuuint32_t estr[2] = {1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE,
-              c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
+                       : (c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B),
               CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -222,7 +223,11 @@ cudaError_t launch_prefill(const awq::kv::dec::Args &P, int64_t most_rows, void 
     A.part_ml = static_cast<float *>(ws);
     A.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + pre_ml_bytes());
     A.timeout_ns = P.timeout_ns;
-    e = launch_overlapped(kernel, dim3((unsigned)(items * splits)), awq::kv::pre::THREADS, S::BYTES, st,
+    A.box_rows = std::min(P.C.page, awq::kv::pre::TILE);
+    CUtensorMap mk, mv;
+    if (!encode_kv_map(&mk, P.C.codes[0], P.C, A.box_rows, false) || !encode_kv_map(&mv, P.C.codes[1], P.C, A.box_rows, false))
+        return cudaErrorInvalidValue;
+    e = launch_overlapped(kernel, dim3((unsigned)(items * splits)), awq::kv::pre::THREADS, S::BYTES, st, mk, mv,
                           (const awq::kv::pre::Args)A);
     if (e != cudaSuccess || splits == 1) return e;
     const int64_t warps = P.T * P.q.heads;

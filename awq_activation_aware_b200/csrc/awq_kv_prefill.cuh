@@ -9,12 +9,12 @@
 //   warps 0-3, 4-7   softmax of tile 0, tile 1: one row a thread.  Scores S from tensor
 //                    memory, P' = 2^(x + e - base) as fp16 back into the columns S came
 //                    from, the row's sum and reference in registers.
-//   warps 8-11       codes to fp16 operands: 16 codes a load, one tile ahead in
-//                    registers, exact conversion, 128-byte-swizzled tiles in shared
-//                    memory.  One conversion serves 256 rows.
+//   warps 8-11       codes to fp16 operands, exactly, in 128-byte-swizzled tiles in
+//                    shared memory.  One conversion serves 256 rows.
 //   warps 12, 13     issue the products of tile 0, tile 1: S = Q K^T from shared memory,
 //                    O += P' V with P' from tensor memory and V [key][D] as it lies in
 //                    the cache (the operand whose rows run along D).
+//   warp 14          brings the codes by TMA, a box per page, and the scales.
 //
 // The scores of a row tile have two buffers of 64 keys: those of the next step are ready
 // when a step's P' is, so the softmax warps never wait for their own products (with one
@@ -47,19 +47,23 @@ using dec::pack_f16;
 constexpr int ROWS = 256, TILE = 128;      // query rows of a block of threads, keys per converted tile
 constexpr int STEP = 64;                   // keys per softmax step
 constexpr int SOFT_WARPS = 8, CONV_WARP = 8, MMA_WARP = 12;
-constexpr int THREADS = 32 * 16;          // warps 14, 15 only give their registers away
+constexpr int THREADS = 32 * 16;          // warp 15 only gives its registers away
 constexpr int SOFT_REGS = 176, CONV_REGS = 104, MMA_REGS = 56;     // of 128 a thread at launch
 static_assert(2 * SOFT_REGS + CONV_REGS + MMA_REGS == 4 * 128, "the block's registers");
+constexpr int LOAD_WARP = 14;
 constexpr int SLOTS = 4;                   // tiles whose scales are kept
+constexpr int RING = 3;                    // operands, and tiles of codes, on the way
 
 template <int D> struct Shape {
     static constexpr int OPERAND = TILE * D * 2;           // one tile of Q, K or V as fp16
-    static constexpr int OFF_Q = 0, OFF_K = 2 * OPERAND, OFF_V = 4 * OPERAND;
-    static constexpr int OFF_SC = 6 * OPERAND;             // float4 [SLOTS][8]: key scale, e, 2^-e of a block's values
+    static constexpr int CODES = TILE * D;                 // one tile of codes
+    static constexpr int OFF_Q = 0, OFF_OP = 2 * OPERAND;  // operands: K and V of a tile in turn, RING of them
+    static constexpr int OFF_RAW = OFF_OP + RING * OPERAND;        // codes as they come
+    static constexpr int OFF_SC = OFF_RAW + RING * CODES;  // float4 [SLOTS][8]: key scale, e, 2^-e of a block's values
     static constexpr int OFF_NAN = OFF_SC + SLOTS * 8 * 16;        // byte [SLOTS][TILE]: the key's values hold a NaN
     static constexpr int OFF_BAR = OFF_NAN + SLOTS * TILE;
-    static constexpr int OFF_ROWS = OFF_BAR + 256;         // int [4][8]: first rows of a tile's blocks in the pool, per warp
-    static constexpr int BYTES = OFF_ROWS + 128 + 1024;    // + alignment
+    static constexpr int OFF_HERE = OFF_BAR + 256;         // int [RING]: which blocks of the codes are there
+    static constexpr int BYTES = OFF_HERE + 16 + 1024;     // + alignment
 };
 
 struct Args {
@@ -71,6 +75,7 @@ struct Args {
     int64_t window;
     float *lse;
     int group, splits, max_tokens;
+    int box_rows;                          // keys per TMA box: min(page, TILE)
     float *part_ml;                        // [block][ROWS][2]
     float *part_o;                         // [block][ROWS][D]
     uint64_t timeout_ns;
@@ -238,13 +243,14 @@ template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setma
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 template <typename TQ, int D>
-__global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
+__global__ void __launch_bounds__(THREADS, 1)
+kv_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const Args A) {
     using S = Shape<D>;
     extern __shared__ uint8_t raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::OFF_BAR);
-    uint64_t *qfull = bars, *kfull = bars + 2, *kempty = bars + 4, *vfull = bars + 6, *vempty = bars + 8, *sfull = bars + 10,
-             *pfull = bars + 14, *pvdone = bars + 18, *drain = bars + 20;      // sfull, pfull: [tile][buffer]
+    uint64_t *qfull = bars, *sfull = bars + 2, *pfull = bars + 6, *pvdone = bars + 10, *drain = bars + 12,     // sfull, pfull: [tile][buffer]
+             *full = bars + 14, *empty = bars + 17, *rawfull = bars + 20, *rawempty = bars + 23;               // [RING]
     __shared__ uint32_t tmem_base_sm;
     __shared__ int abort_sm;
     volatile int *abort_flag = &abort_sm;
@@ -254,12 +260,14 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
         abort_sm = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(qfull + i, 128);
-            mbar_init(kfull + i, 128);
-            mbar_init(kempty + i, 2);
-            mbar_init(vfull + i, 128);
-            mbar_init(vempty + i, 2);
             mbar_init(pvdone + i, 1);
             mbar_init(drain + i, 1);
+        }
+        for (int i = 0; i < RING; ++i) {
+            mbar_init(full + i, 128);
+            mbar_init(empty + i, 2);
+            mbar_init(rawfull + i, 1);
+            mbar_init(rawempty + i, 4);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(sfull + i, 1);
@@ -373,14 +381,15 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                     tmem_st_32x32b_x32(s_tmem + 64 * buf, p);
                     l += add;
                     if (!whole) {                          // NaN values were taken out of the product: into the sums of who sees them
-                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(vfull + ((j >> 1) & 1), (j >> 2) & 1, abort_flag, A.timeout_ns));
+                        const int n = 2 * (j >> 1) + 1;    // the values' place in the ring
+                        ok = __all_sync(0xffffffffu, mbar_wait_bounded(full + n % RING, (n / RING) & 1, abort_flag, A.timeout_ns));
                         const uint32_t *bad = reinterpret_cast<const uint32_t *>(sm + S::OFF_NAN + slot * TILE + buf * STEP);
                         for (int k = 0; k < STEP / 4; ++k) {
                             const uint32_t x = bad[k];
                             if (!x) continue;
-                            for (int n = 0; n < 4; ++n) {
-                                const int key = key0 + 4 * k + n;
-                                if (((x >> (8 * n)) & 1) && key >= row_lo && key < row_hi) l = NAN;
+                            for (int i = 0; i < 4; ++i) {
+                                const int key = key0 + 4 * k + i;
+                                if (((x >> (8 * i)) & 1) && key >= row_lo && key < row_hi) l = NAN;
                             }
                         }
                     }
@@ -433,52 +442,47 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
             }
         } else if (warp < MMA_WARP) {
             regs_down<CONV_REGS>();
-            // ---- codes to operands: scales and keys of a tile, then its values (keys first: the scores run ahead)
-            constexpr int PER = D / 16;                            // 16-byte chunks of codes a row, and loads a thread
-            constexpr int SKIP = 128 / PER;                            // rows between a thread's loads
+            // ---- codes to operands: keys, then values of each tile (keys first: the scores run ahead)
+            constexpr int PER = D / 16;                            // 16-byte chunks of codes a row, and of a thread
+            constexpr int SKIP = 128 / PER;                        // rows between a thread's chunks
             const int t = threadIdx.x - 32 * CONV_WARP, chunk = t % PER, r0 = t / PER;
-            const int page_bits = 31 - __clz(A.C.page);
-            if (t == 0 && w.s.len > (A.B.max_pages * A.C.page < kMaxLen ? A.B.max_pages * A.C.page : kMaxLen))
-                atomicOr(&g_dev_error, kDevErrBadIndex);
-            // first row of block `lane` (of 8) of a tile in the pool; -1: no such keys, or a bad page
-            auto block_rows = [&](int it) -> int {
-                const int pos = (w.t0 + it) * TILE + 16 * lane;
-                if (lane >= 8 || it >= w.nt || pos >= w.hi) return -1;
-                const int64_t page = A.B.pages[(int64_t)w.b * A.B.ld_pages + (pos >> page_bits)];
-                if (page < 0 || page >= A.C.n_pages) {
-                    atomicOr(&g_dev_error, kDevErrBadIndex);
-                    return -1;
-                }
-                return (int)((page * A.C.heads + w.head) * A.C.page) + (pos & (A.C.page - 1));
-            };
-            // this thread's rows of a tile: block first rows through shared memory, then one load each
-            int *mine8 = reinterpret_cast<int *>(sm + S::OFF_ROWS) + 8 * (warp - CONV_WARP);
-            auto rows_of = [&](int rows, int (&at)[PER]) {
+            bool ok = true;
+            for (int n = 0; n < 2 * w.nt && ok; ++n) {
+                const int st = n % RING, key0 = (w.t0 + n / 2) * TILE;
+                const uint32_t ph = (n / RING) & 1;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(rawfull + st, ph, abort_flag, A.timeout_ns));
+                if (!ok) break;
+                const uint32_t src = smem_u32(sm + S::OFF_RAW + st * S::CODES) + 16 * t;
+                const int here = *reinterpret_cast<const volatile int *>(sm + S::OFF_HERE + 4 * st);
+                uint4 v[PER];
+#pragma unroll
+                for (int i = 0; i < PER; ++i) v[i] = dec::lds128(src + 2048 * i);      // rows r0 + SKIP i lie 2048 bytes apart
                 __syncwarp();
-                if (lane < 8) mine8[lane] = rows;
-                __syncwarp();
+                if (lane == 0) mbar_arrive(rawempty + st);
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty + st, ph ^ 1, abort_flag, A.timeout_ns));
+                if (!ok) break;
+                const bool whole = whole_tile(w, key0);
+                if (!whole || here != 255) {
 #pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    const int row = r0 + SKIP * i, first = mine8[row / 16];
-                    at[i] = first < 0 ? -1 : first + row % 16;
+                    for (int i = 0; i < PER; ++i) {
+                        const int row = r0 + SKIP * i;
+                        const bool gone = !((here >> (row / 16)) & 1) || key0 + row >= w.hi;
+                        uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w}, any = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (gone) x[k] = 0;
+                            if (!whole && (n & 1)) {               // NaN values: out of the product (see soft_step's caller)
+                                const uint32_t nan = nan_bytes(x[k]);
+                                any |= nan;
+                                x[k] &= ~((nan >> 7) * 0xffu);
+                            }
+                        }
+                        v[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        const uint32_t votes = __ballot_sync(0xffffffffu, any != 0);
+                        if (chunk == 0 && (n & 1))
+                            sm[S::OFF_NAN + (n / 2 % SLOTS) * TILE + row] = (votes >> (lane & ~(PER - 1))) & ((1u << PER) - 1) ? 1 : 0;
+                    }
                 }
-            };
-            auto load = [&](const uint8_t *codes, const int (&at)[PER], uint4 (&v)[PER]) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) {
-                    v[i] = make_uint4(0, 0, 0, 0);
-                    if (at[i] >= 0) v[i] = ldg_stream_v4(codes + (int64_t)at[i] * D + 16 * chunk);
-                }
-            };
-            // lanes 0-7 the key scale of a block, 8-15 its value scale; -1 where there is none
-            auto load_scale = [&](int rows) {
-                const int first = __shfl_sync(0xffffffffu, rows, lane & 7);
-                return lane < 16 && first >= 0 ? A.C.scales[lane >> 3][first / 16] : -1.0f;
-            };
-            // the conversions stay behind the wait before them: hoisted above it they wait for the loads
-            auto store = [&](uint8_t *dst, uint4 (&v)[PER]) {
-#pragma unroll
-                for (int i = 0; i < PER; ++i) asm volatile("" : "+r"(v[i].x), "+r"(v[i].y), "+r"(v[i].z), "+r"(v[i].w));
 #pragma unroll
                 for (int i = 0; i < PER; ++i) {
                     const int row = r0 + SKIP * i;
@@ -487,69 +491,16 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                     const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                     const uint4 lo = make_uint4(cvt_lo(x[0]), cvt_hi(x[0]), cvt_lo(x[1]), cvt_hi(x[1]));
                     const uint4 hi = make_uint4(cvt_lo(x[2]), cvt_hi(x[2]), cvt_lo(x[3]), cvt_hi(x[3]));
-                    const uint32_t half = smem_u32(dst) + (chunk / 4) * (TILE * 128), c = 2 * (chunk % 4);
+                    const uint32_t half = smem_u32(sm + S::OFF_OP + st * S::OPERAND) + (chunk / 4) * (TILE * 128), c = 2 * (chunk % 4);
                     const bool swap = (chunk / 4) & 1;
                     st_shared_v4(half + sw128_offset(row, c + swap), swap ? hi : lo);
                     st_shared_v4(half + sw128_offset(row, c + 1 - swap), swap ? lo : hi);
                 }
-            };
-            bool ok = true;
-            uint4 kc[PER], vc[PER];
-            int rows = block_rows(0);
-            int at[PER];
-            rows_of(rows, at);
-            load(A.C.codes[1], at, vc);
-            load(A.C.codes[0], at, kc);
-            float scale = load_scale(rows);
-            rows = block_rows(1);
-            for (int it = 0; it < w.nt && ok; ++it) {
-                const int st = it & 1, key0 = (w.t0 + it) * TILE, slot = it % SLOTS;
-                const uint32_t ph = ((it >> 1) & 1) ^ 1;
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(kempty + st, ph, abort_flag, A.timeout_ns));
-                if (!ok) break;
-                if (warp == CONV_WARP) {
-                    const float vs = __shfl_sync(0xffffffffu, scale, (lane & 7) + 8);
-                    if (lane < 8) {
-                        const uint32_t bits = __float_as_uint(vs);
-                        float4 q = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);
-                        if (scale >= 0.0f && vs >= 0.0f)
-                            q = make_float4(scale, (float)((int)(bits >> 23) - 127), __uint_as_float(0x7f000000u - bits), 0.0f);
-                        reinterpret_cast<float4 *>(sm + S::OFF_SC)[slot * 8 + lane] = q;
-                    }
-                }
-                store(sm + S::OFF_K + st * S::OPERAND, kc);
                 fence_proxy_async_smem();
-                mbar_arrive(kfull + st);
-                rows_of(rows, at);
-                load(A.C.codes[0], at, kc);
-                scale = load_scale(rows);
-                rows = block_rows(it + 2);
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(vempty + st, ph, abort_flag, A.timeout_ns));
-                if (!ok) break;
-                if (!whole_tile(w, key0)) {
-#pragma unroll
-                    for (int i = 0; i < PER; ++i) {
-                        const int row = r0 + SKIP * i;
-                        uint32_t x[4] = {vc[i].x, vc[i].y, vc[i].z, vc[i].w}, any = 0;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (key0 + row >= w.hi) x[k] = 0;
-                            const uint32_t nan = nan_bytes(x[k]);
-                            any |= nan;
-                            x[k] &= ~((nan >> 7) * 0xffu);
-                        }
-                        vc[i] = make_uint4(x[0], x[1], x[2], x[3]);
-                        const uint32_t votes = __ballot_sync(0xffffffffu, any != 0);
-                        if (chunk == 0)
-                            sm[S::OFF_NAN + slot * TILE + row] = (votes >> (lane & ~(PER - 1))) & ((1u << PER) - 1) ? 1 : 0;
-                    }
-                }
-                store(sm + S::OFF_V + st * S::OPERAND, vc);
-                fence_proxy_async_smem();
-                mbar_arrive(vfull + st);
-                load(A.C.codes[1], at, vc);
+                mbar_arrive(full + st);
             }
-        } else if (regs_down<MMA_REGS>(); warp < MMA_WARP + tiles && w.nt > 0) {
+        } else if (regs_down<MMA_REGS>(); w.nt == 0) {
+        } else if (warp < MMA_WARP + tiles) {
             // ---- the products of one tile: its O += P' V, then its next scores.  The whole warp runs along and one
             // lane issues, so that addresses stay warp-uniform; with one warp for both tiles, issuing from a
             // single-lane branch, an instruction took 190 clocks to leave (64 is what it computes).
@@ -557,7 +508,7 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
             const int t = warp - MMA_WARP;
             const bool leader = elect_one();
             const uint32_t base = __shfl_sync(0xffffffffu, smem_u32(sm), 0) >> 4, tm = __shfl_sync(0xffffffffu, tmem, 0);
-            const uint32_t q_lo = base + ((S::OFF_Q + t * S::OPERAND) >> 4), k_lo = base + (S::OFF_K >> 4), v_lo = base + (S::OFF_V >> 4);
+            const uint32_t q_lo = base + ((S::OFF_Q + t * S::OPERAND) >> 4), op_lo = base + (S::OFF_OP >> 4);
             const uint32_t s_tmem = tm + 128 * t, o_tmem = tm + 256 + 128 * t;
             bool ok = true;
             auto wait = [&](uint64_t *bar, uint32_t ph) {
@@ -569,19 +520,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
                 if (tiles == 1) mma_commit_1(bar);
             };
             auto scores = [&](int j) {                             // of step j, into the buffer that P'(j - 2) leaves
-                const int st = (j >> 1) & 1, buf = j & 1;
-                if (buf == 0) wait(kfull + st, (j >> 2) & 1);
+                const int n = 2 * (j >> 1), st = n % RING, buf = j & 1;
+                if (buf == 0) wait(full + st, (n / RING) & 1);
                 if (!ok) return;
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t b = k_lo + st * (S::OPERAND >> 4) + buf * ((STEP * 128) >> 4);
+                    const uint32_t b = op_lo + st * (S::OPERAND >> 4) + buf * ((STEP * 128) >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         const uint32_t off = ((k / 4) * TILE * 128 + (k % 4) * 32) >> 4;
                         mma_ss<kDescK>(s_tmem + 64 * buf, q_lo + off, b + off, QK, k > 0);
                     }
                     mma_commit_1(sfull + 2 * t + buf);
-                    if (buf || j + 1 == w.ns) release(kempty + st);
+                    if (buf || j + 1 == w.ns) release(empty + st);
                 }
                 __syncwarp();
             };
@@ -589,19 +540,19 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
             scores(0);
             if (w.ns > 1) scores(1);
             for (int j = 0; j < w.ns && ok; ++j) {
-                const int st = (j >> 1) & 1, buf = j & 1;
-                if (buf == 0) wait(vfull + st, (j >> 2) & 1);
+                const int n = 2 * (j >> 1) + 1, st = n % RING, buf = j & 1;
+                if (buf == 0) wait(full + st, (n / RING) & 1);
                 wait(pfull + 2 * t + buf, (j >> 1) & 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (leader) {
-                    const uint32_t b = v_lo + st * (S::OPERAND >> 4) + buf * ((STEP * 128) >> 4);
+                    const uint32_t b = op_lo + st * (S::OPERAND >> 4) + buf * ((STEP * 128) >> 4);
                     mma_ts<kDescV>(o_tmem, s_tmem + 64 * buf, b, PV, j > 0);
 #pragma unroll
                     for (int k = 1; k < STEP / 16; ++k)
                         mma_ts<kDescV>(o_tmem, s_tmem + 64 * buf + 8 * k, b + ((k * 2048) >> 4), PV, true);
                     mma_commit_1(pvdone + t);
-                    if (buf || j + 1 == w.ns) release(vempty + st);
+                    if (buf || j + 1 == w.ns) release(empty + st);
                 }
                 __syncwarp();
                 if (j + 2 < w.ns) scores(j + 2);
@@ -609,6 +560,66 @@ __global__ void __launch_bounds__(THREADS, 1) kv_prefill_kernel(const Args A) {
             if (leader) mma_commit_1(drain + t);                   // every product this thread issued has finished when this fires
             __syncwarp();
             mbar_wait_bounded(drain + t, 0, abort_flag, A.timeout_ns);
+        } else if (warp == LOAD_WARP) {
+            // ---- codes and scales, up to RING tiles ahead; a lane looks after a block of 16 keys (of eight)
+            const int page_bits = 31 - __clz(A.C.page), per_box = A.box_rows / kBlock;
+            if (lane == 0 && w.s.len > (A.B.max_pages * A.C.page < kMaxLen ? A.B.max_pages * A.C.page : kMaxLen))
+                atomicOr(&g_dev_error, kDevErrBadIndex);
+            // first row of block `lane & 7` of a tile in the pool; -1: no such keys, or a bad page
+            auto page_at = [&](int it) -> int64_t {
+                const int pos = (w.t0 + it) * TILE + 16 * (lane & 7);
+                return it < w.nt && pos < w.hi ? A.B.pages[(int64_t)w.b * A.B.ld_pages + (pos >> page_bits)] : 0;
+            };
+            auto row_at = [&](int it, int64_t page) -> int {
+                const int pos = (w.t0 + it) * TILE + 16 * (lane & 7);
+                if (it >= w.nt || pos >= w.hi) return -1;
+                if (page < 0 || page >= A.C.n_pages) {
+                    atomicOr(&g_dev_error, kDevErrBadIndex);
+                    return -1;
+                }
+                return (int)((page * A.C.heads + w.head) * A.C.page) + (pos & (A.C.page - 1));
+            };
+            auto scale_at = [&](int row) { return lane < 16 && row >= 0 ? A.C.scales[lane >> 3][row / 16] : -1.0f; };   // 0-7 keys, 8-15 values
+            bool ok = true;
+            int row = row_at(0, page_at(0));
+            float scale = scale_at(row);
+            int64_t page = page_at(1);
+            int n = 0;
+            for (; n < 2 * w.nt && ok; ++n) {
+                const int st = n % RING, it = n / 2;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(rawempty + st, ((n / RING) & 1) ^ 1, abort_flag, A.timeout_ns));
+                if (!ok) break;
+                const uint32_t here = __ballot_sync(0xffffffffu, row >= 0) & 255;
+                const bool box = lane < 8 && row >= 0 && lane % per_box == 0;
+                const int boxes = __popc(__ballot_sync(0xffffffffu, box));
+                if ((n & 1) == 0) {
+                    const float vs = __shfl_sync(0xffffffffu, scale, (lane & 7) + 8);
+                    if (lane < 8) {
+                        const uint32_t bits = __float_as_uint(vs);
+                        float4 q = make_float4(0.0f, -INFINITY, 1.0f, 0.0f);       // a block that is not there: hidden
+                        if (row >= 0) q = make_float4(scale, (float)((int)(bits >> 23) - 127), __uint_as_float(0x7f000000u - bits), 0.0f);
+                        reinterpret_cast<float4 *>(sm + S::OFF_SC)[(it % SLOTS) * 8 + lane] = q;
+                    }
+                }
+                if (lane == 0) *reinterpret_cast<volatile int *>(sm + S::OFF_HERE + 4 * st) = (int)here;
+                __syncwarp();
+                if (lane == 0) mbar_arrive_expect_tx(rawfull + st, boxes * A.box_rows * D);
+                __syncwarp();
+                if (box)
+                    tma_load_2d(sm + S::OFF_RAW + st * S::CODES + lane * kBlock * D, n & 1 ? &tmap_v : &tmap_k, 0, row, rawfull + st);
+                if (n & 1) {                                       // on to the next tile; the page numbers after it are on their way
+                    row = row_at(it + 1, page);
+                    scale = scale_at(row);
+                    page = page_at(it + 2);
+                }
+            }
+            if (!ok) {                                             // given up: let the copies in flight land
+                for (int k = n > RING ? n - RING : 0; k < n; ++k) {
+                    const uint64_t t0 = global_timer_ns();
+                    while (!mbar_try_wait_hint(rawfull + k % RING, (k / RING) & 1, 20000u))
+                        if (global_timer_ns() - t0 > A.timeout_ns) break;
+                }
+            }
         }
     }
     __syncwarp();
