@@ -159,6 +159,21 @@ __device__ __forceinline__ void store_n(T *p, const float (&v)[N]) {
     for (int i = 0; i < N / M; ++i) reinterpret_cast<W *>(p)[i] = w[i];
 }
 
+// N elements as they lie in memory, to be taken apart later (fewer registers while they are on their way).
+template <typename T, int N> struct Raw {
+    static constexpr int B = sizeof(T) * N < 16 ? sizeof(T) * N : 16, M = sizeof(T) * N / B;
+    typename Word<B>::type w[M];
+    __device__ __forceinline__ void load(const T *p) {
+#pragma unroll
+        for (int i = 0; i < M; ++i) w[i] = reinterpret_cast<const typename Word<B>::type *>(p)[i];
+    }
+    __device__ __forceinline__ void take(float (&v)[N]) const {
+        const T *t = reinterpret_cast<const T *>(w);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = to_f(t[i]);
+    }
+};
+
 // ---------------------------------------------------------------------------
 // The table of cosines and sines.  Angles pos * f_i and the frequencies
 // f_i = base^(-2 i / rot), in binary64: at position 10^5 a binary32 angle is off
@@ -196,10 +211,13 @@ __device__ __forceinline__ float2 rotate(float x1, float x2, float2 cs) {
 }
 
 // ---------------------------------------------------------------------------
-// Rotary positions of rows [T][heads][dim].  Bound by the bytes of x and y; the
-// table's row of a token is read once per head from L1.  One block per token;
-// a thread moves 8 neighbouring elements (16 with their partners in the half
-// layout), or one pair where alignment or sizes do not allow 16-byte accesses.
+// Rotary positions of rows [T][heads][dim].  Bound by the bytes of x and y.  One block
+// of threads per token; a thread keeps to one place of the head -- 8 neighbouring
+// elements, with their 8 partners in the half layout, or one pair where alignment or
+// sizes do not allow 16-byte accesses -- loads its cosines and sines once and goes over
+// the heads, two of them on their way at a time, the first two before the position is known.
+// Few registers (64 at most, so 1024 threads an SM) matter more than loads in flight: with
+// four heads in 128 registers 16384 tokens of 32 heads took 203 us instead of 65.
 // ---------------------------------------------------------------------------
 struct RopeArgs {
     Rows x, y;
@@ -217,96 +235,118 @@ __device__ __forceinline__ void load_cs(const float2 *row, float sign, float2 (&
         cs[2 * i + 1] = make_float2(v.z, v.w * sign);
     }
 }
-// Item `i` of one head's row: rows of items are [rot / 16] of paired eights
-// (half layout) or [rot / 8] of four pairs (interleaved), then [(dim - rot) / 8] eights.
-template <typename TI, typename TO>
-__device__ __forceinline__ void rope_item(const TI *x, TO *y, const float2 *row, const Rope &r, float sign, int i) {
-    const int half = r.rot >> 1;
-    if (r.interleaved) {
-        float v[8];
-        load_n(x + 8 * i, v);
-        if (8 * i < r.rot) {
-            float2 cs[4];
-            load_cs(row + 4 * i, sign, cs);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float2 z = rotate(v[2 * j], v[2 * j + 1], cs[j]);
-                v[2 * j] = z.x;
-                v[2 * j + 1] = z.y;
-            }
-        }
-        store_n(y + 8 * i, v);
-    } else if (16 * i < r.rot) {
-        float a[8], b[8];
-        float2 cs[8];
-        load_n(x + 8 * i, a);
-        load_n(x + half + 8 * i, b);
-        load_cs(row + 8 * i, sign, cs);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float2 z = rotate(a[j], b[j], cs[j]);
-            a[j] = z.x;
-            b[j] = z.y;
-        }
-        store_n(y + 8 * i, a);
-        store_n(y + half + 8 * i, b);
-    } else {
-        const int d = r.rot + 8 * (i - (r.rot >> 4));
-        float v[8];
-        load_n(x + d, v);
-        store_n(y + d, v);
-    }
-}
+// Places of a head's row: [rot / 16] paired eights (half layout) or [rot / 8] of four pairs
+// (interleaved), then [(dim - rot) / 8] eights to copy; without 16-byte accesses dim / 2 pairs.
 __host__ __device__ __forceinline__ int rope_items(int dim, int rot, bool interleaved) {
     return interleaved ? dim / 8 : rot / 16 + (dim - rot) / 8;
 }
-// Pair `i` of dim / 2, any alignment.
-template <typename TI, typename TO>
-__device__ __forceinline__ void rope_pair(const TI *x, TO *y, const float2 *row, const Rope &r, float sign, int i) {
-    const int half = r.rot >> 1;
-    int d1 = 2 * i, d2 = 2 * i + 1;
-    if (!r.interleaved && i < half) {
-        d1 = i;
-        d2 = i + half;
+// One head's place, in: MODE 0 eights to copy, 1 four pairs, 2 paired eights.
+template <int MODE, typename TO, typename RX, typename CS>
+__device__ __forceinline__ void rope_place(const RX &ra, const RX &rb, TO *y, int half, const CS &cs) {
+    float a[8], b[8];
+    ra.take(a);
+    if (MODE == 2) rb.take(b);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        if (MODE == 2) {
+            const float2 z = rotate(a[j], b[j], cs[j]);
+            a[j] = z.x;
+            b[j] = z.y;
+        } else if (MODE == 1 && !(j & 1)) {
+            const float2 z = rotate(a[j], a[j + 1], cs[j / 2]);
+            a[j] = z.x;
+            a[j + 1] = z.y;
+        }
     }
-    float2 z = make_float2(to_f(x[d1]), to_f(x[d2]));
-    if (i < half) {
-        float2 cs = row[i];
-        cs.y *= sign;
-        z = rotate(z.x, z.y, cs);
-    }
-    y[d1] = from_f<TO>(z.x);
-    y[d2] = from_f<TO>(z.y);
+    store_n(y, a);
+    if (MODE == 2) store_n(y + half, b);
 }
-template <typename TI, typename TO, bool VEC>
-__global__ void __launch_bounds__(256) rope_kernel(const RopeArgs A) {
+// All heads of one token, by `threads` threads of which this is number `tid`.  `position` is called once, after the
+// first heads' loads are out; it gives the table's row or NULL (nothing is written).
+template <bool INTER, bool VEC, typename TI, typename TO, typename POS>
+__device__ __forceinline__ void rope_token(const TI *x, int64_t ldx, TO *y, int64_t ldy, const Rope &r, float sign, int dim,
+                                           int heads, int tid, int threads, POS position) {
+    const int half = r.rot >> 1, per = VEC ? rope_items(dim, r.rot, INTER) : dim / 2;
+    const int wide = per < threads ? per : threads, step = threads / wide, h0 = tid / wide;
+    if (h0 >= step) return;
+    if constexpr (VEC) {
+        constexpr int U = 2;                                       // heads on their way at a time
+        const float2 *row = nullptr;
+        for (int j = tid % wide; j < per; j += wide) {
+            const bool turn = (INTER ? 8 : 16) * j < r.rot;
+            const int d = INTER || turn ? 8 * j : r.rot + 8 * (j - (r.rot >> 4));
+            const bool two = !INTER && turn;
+            float2 cs[INTER ? 4 : 8];
+            for (int h = h0; h < heads; h += U * step) {
+                Raw<TI, 8> a[U], b[INTER ? 1 : U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (h + u * step < heads) {
+                        a[u].load(x + (h + u * step) * ldx + d);
+                        if (two) b[INTER ? 0 : u].load(x + (h + u * step) * ldx + d + half);
+                    }
+                if (h == h0) {
+                    if (!row) row = position();
+                    if (!row) return;
+                    if (turn) load_cs(row + (INTER ? 4 : 8) * j, sign, cs);
+                }
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (h + u * step < heads) {
+                        TO *to = y + (h + u * step) * ldy + d;
+                        if (!turn) rope_place<0>(a[u], a[u], to, half, cs);
+                        else if (INTER) rope_place<1>(a[u], a[u], to, half, cs);
+                        else rope_place<INTER ? 1 : 2>(a[u], b[INTER ? 0 : u], to, half, cs);
+                    }
+            }
+        }
+    } else {
+        const float2 *row = position();
+        if (!row) return;
+        for (int j = tid % wide; j < per; j += wide) {
+            int d1 = 2 * j, d2 = 2 * j + 1;
+            float2 cs = make_float2(1.0f, 0.0f);
+            if (j < half) {
+                cs = row[j];
+                cs.y *= sign;
+                if (!INTER) {
+                    d1 = j;
+                    d2 = j + half;
+                }
+            }
+            for (int h = h0; h < heads; h += step) {
+                float2 z = make_float2(to_f(x[h * ldx + d1]), to_f(x[h * ldx + d2]));
+                if (j < half) z = rotate(z.x, z.y, cs);
+                y[h * ldy + d1] = from_f<TO>(z.x);
+                y[h * ldy + d2] = from_f<TO>(z.y);
+            }
+        }
+    }
+}
+template <typename TI, typename TO, bool INTER, bool VEC>
+__global__ void __launch_bounds__(256, 4) rope_kernel(const RopeArgs A) {
+    griddep_launch_dependents();
+    griddep_wait();
     const int64_t t = blockIdx.x;
-    const int64_t pos = A.positions[t];
-    if (pos < 0 || pos >= A.r.n_pos) {
-        if (threadIdx.x == 0) atomicOr(&g_dev_error, kDevErrBadIndex);
-        return;
-    }
-    const float2 *row = A.r.table + pos * (A.r.rot >> 1);
-    const float sign = A.inverse ? -1.0f : 1.0f;
-    const TI *x = static_cast<const TI *>(A.x.data) + t * A.x.ld_tok;
-    TO *y = static_cast<TO *>(const_cast<void *>(A.y.data)) + t * A.y.ld_tok;
-    const int per = VEC ? rope_items(A.dim, A.r.rot, A.r.interleaved) : A.dim / 2;
-    for (int i = threadIdx.x; i < per * A.x.heads; i += blockDim.x) {
-        const int h = i / per, j = i - h * per;
-        if (VEC) rope_item(x + h * A.x.ld_head, y + h * A.y.ld_head, row, A.r, sign, j);
-        else rope_pair(x + h * A.x.ld_head, y + h * A.y.ld_head, row, A.r, sign, j);
-    }
+    rope_token<INTER, VEC>(static_cast<const TI *>(A.x.data) + t * A.x.ld_tok, A.x.ld_head,
+                           static_cast<TO *>(const_cast<void *>(A.y.data)) + t * A.y.ld_tok, A.y.ld_head, A.r,
+                           A.inverse ? -1.0f : 1.0f, A.dim, A.x.heads, threadIdx.x, blockDim.x, [&]() -> const float2 * {
+                               const int64_t pos = A.positions[t];
+                               if (pos >= 0 && pos < A.r.n_pos) return A.r.table + pos * (A.r.rot >> 1);
+                               atomicOr(&g_dev_error, kDevErrBadIndex);
+                               return nullptr;
+                           });
 }
 
 // ---------------------------------------------------------------------------
-// Append.  One warp per (block of 16 positions that gets new tokens, head, keys
-// or values): all new rows of the block are held in registers (16 x D / 32 values
-// a lane), so k and v are read once, the block's exponent is known before any
-// code is written, and no two warps touch the same block.  Bound by the bytes of
-// k and v; in decode (one row a block) by latency.
+// Append.  A team of warps per (block of 16 positions that gets new tokens, head, keys or
+// values): four warps of four rows each, whose values stay in registers, so k and v are
+// read once, the block's exponent is known before any code is written, and no two teams
+// touch the same block; one warp and one row where every sequence has one new token.
+// Bound by the bytes of k, v and q; in decode by latency.
 // Rows are dealt to blocks of threads in chunks: the rows of a chunk that open a
 // block (its leaders) are found by a ballot, and (leader, head, k / v) items go
-// round the warps.  A second range of the grid rotates the queries.
+// round the teams.  A second range of the grid rotates the queries.
 // ---------------------------------------------------------------------------
 struct AppendArgs {
     Cache C;
@@ -314,7 +354,6 @@ struct AppendArgs {
     int64_t T;
     Rows kv[2], q, q_out;
     Rope r;                    // table NULL: no rotation
-    int chunk;                 // rows per block of threads: 1 or 16
     int64_t chunks;            // blocks in x that append; those past them rotate queries
 };
 constexpr int kAppendThreads = 256;
@@ -328,9 +367,20 @@ __device__ __forceinline__ int64_t last_position(const Batch &B, const Cache &C,
 template <typename TI, int N>
 __device__ __forceinline__ void rotated(const TI *x, const float2 *row, const Rope &r, int d0, float (&v)[N]) {
     load_n(x + d0, v);
-    if (!row) return;
+    if (!row || d0 >= r.rot) return;
     const int half = r.rot >> 1;
     if (r.interleaved) {
+        if (N == 4 && half % 2 == 0 && d0 + N <= r.rot) {          // two pairs: one 16-byte load of the table
+            float2 cs[2];
+            load_cs(row + (d0 >> 1), 1.0f, cs);
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                const float2 z = rotate(v[j], v[j + 1], cs[j / 2]);
+                v[j] = z.x;
+                v[j + 1] = z.y;
+            }
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < N; j += 2) {
             if (d0 + j >= r.rot) continue;
@@ -338,6 +388,14 @@ __device__ __forceinline__ void rotated(const TI *x, const float2 *row, const Ro
             v[j] = z.x;
             v[j + 1] = z.y;
         }
+    } else if (half % N == 0 && half % 2 == 0) {                   // the lane's elements have N neighbouring partners
+        const bool hi = d0 >= half;
+        float o[N];
+        float2 cs[N];
+        load_n(x + (hi ? d0 - half : d0 + half), o);
+        load_cs(row + (hi ? d0 - half : d0), 1.0f, cs);
+#pragma unroll
+        for (int j = 0; j < N; ++j) v[j] = hi ? rotate(o[j], v[j], cs[j]).y : rotate(v[j], o[j], cs[j]).x;
     } else {
 #pragma unroll
         for (int j = 0; j < N; ++j) {
@@ -371,98 +429,112 @@ __device__ __forceinline__ void store_codes(uint8_t *p, const float (&v)[N], flo
     else *reinterpret_cast<uint16_t *>(p) = w[0];
 }
 
-template <typename TI, int D>
-__device__ __forceinline__ void append_block(const AppendArgs &A, const Seq &s, int b, int64_t pos, int64_t row,
-                                             int head, int which) {
-    constexpr int N = D / 32;
+// One item.  TEAM warps (this is number `member`) with kBlock / TEAM rows each, or one with one row.
+template <typename TI, int D, int TEAM>
+__device__ __forceinline__ void append_block(const AppendArgs &A, int64_t len, int b, int64_t pos, int64_t row, int head,
+                                             int which, int member, int team, float *share) {
+    constexpr int N = D / 32, OWN = TEAM == 1 ? 1 : kBlock / TEAM;
     const int lane = threadIdx.x & 31, d0 = lane * N;
     const int64_t end = last_position(A.B, A.C, A.r);
     const int off = (int)(pos % kBlock);                           // rows of the block from before
-    const int64_t page = page_of(A.B, A.C, b, pos);
+    const int64_t page = page_of(A.B, A.C, b, pos);                // the same for the whole team
     if (page < 0) return;
     int n = kBlock - off;
-    if (s.len - pos < n) n = (int)(s.len - pos);
+    if (len - pos < n) n = (int)(len - pos);
     if (end - pos < n) n = (int)(end - pos);
     const Rows &R = A.kv[which];
     const TI *x = static_cast<const TI *>(R.data) + row * R.ld_tok + head * R.ld_head;
     const int half = A.r.rot >> 1;
     const bool turn = which == 0 && A.r.table != nullptr;
-    float v[kBlock][N];
+    const int64_t tile = (page * A.C.heads + head) * A.C.page + pos % A.C.page;     // first row written
+    float *scale = A.C.scales[which] + tile / kBlock;
+    uint8_t *codes = A.C.codes[which] + tile * D + d0;
+    const int e_old = off ? exponent_of(*scale) : kEMin;
+    float v[OWN][N];
     float amax = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kBlock; ++i)
-        if (i < n) rotated<TI, N>(x + i * R.ld_tok, turn ? A.r.table + (pos + i) * half : nullptr, A.r, d0, v[i]);
+    for (int i = 0; i < OWN; ++i) {
+        const int k = member * OWN + i;
+        if (k < n) rotated<TI, N>(x + k * R.ld_tok, turn ? A.r.table + (pos + k) * half : nullptr, A.r, d0, v[i]);
+    }
 #pragma unroll
-    for (int i = 0; i < kBlock; ++i)
-        if (i < n) {
+    for (int i = 0; i < OWN; ++i)
+        if (member * OWN + i < n) {
 #pragma unroll
             for (int j = 0; j < N; ++j)
                 if (isfinite(v[i][j])) amax = fmaxf(amax, fabsf(v[i][j]));
         }
-    int e = exponent_for(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax))));
-    const int64_t tile = (page * A.C.heads + head) * A.C.page + pos % A.C.page;     // first row written
-    float *scale = A.C.scales[which] + tile / kBlock;
-    uint8_t *codes = A.C.codes[which] + tile * D + d0;
-    if (off) {
-        const int e_old = exponent_of(*scale);
-        if (e > e_old) {
-            const float f = pow2(e_old - e);
-            for (int i = 1; i <= off; ++i) {
-                uint8_t *p = codes - i * D;
-                uint16_t w[N / 2];
-#pragma unroll
-                for (int j = 0; j < N / 2; ++j) {
-                    const float2 o = from_e4m3x2(reinterpret_cast<const uint16_t *>(p)[j]);
-                    w[j] = e4m3x2(o.x * f, o.y * f);
-                }
-#pragma unroll
-                for (int j = 0; j < N / 2; ++j) reinterpret_cast<uint16_t *>(p)[j] = w[j];
-            }
-        } else {
-            e = e_old;
-        }
-        __syncwarp();                                              // every lane has read the old scale
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+    if (TEAM > 1) {
+        if (lane == 0) share[member] = amax;
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * TEAM) : "memory");       // every warp has read the old scale, too
+        amax = fmaxf(fmaxf(share[0], share[1]), fmaxf(share[2], share[3]));
+    } else {
+        __syncwarp();
     }
-    if (lane == 0) *scale = pow2(e);
+    int e = exponent_for(amax);
+    if (e > e_old) {
+        const float f = pow2(e_old - e);
+        for (int i = 1 + member; i <= off; i += TEAM) {            // the codes from before, in the new scale
+            uint8_t *p = codes - i * D;
+            uint16_t w[N / 2];
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) {
+                const float2 o = from_e4m3x2(reinterpret_cast<const uint16_t *>(p)[j]);
+                w[j] = e4m3x2(o.x * f, o.y * f);
+            }
+#pragma unroll
+            for (int j = 0; j < N / 2; ++j) reinterpret_cast<uint16_t *>(p)[j] = w[j];
+        }
+    } else {
+        e = e_old;
+    }
+    if (lane == 0 && member == 0) *scale = pow2(e);
     const float inv = pow2(-e);
 #pragma unroll
-    for (int i = 0; i < kBlock; ++i)
-        if (i < n) store_codes<N>(codes + i * D, v[i], inv);
+    for (int i = 0; i < OWN; ++i)
+        if (member * OWN + i < n) store_codes<N>(codes + (member * OWN + i) * D, v[i], inv);
 }
 
-template <typename TI, typename TO, int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs A) {
+template <typename TI, typename TO, int D, int TEAM>
+__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendArgs A) {
+    constexpr int CHUNK = TEAM == 1 ? 1 : 16, WARPS = kAppendThreads / 32, TEAMS = WARPS / TEAM;
+    __shared__ float share[TEAMS][2][4];
+    griddep_launch_dependents();
+    griddep_wait();
     const int64_t end = last_position(A.B, A.C, A.r);
     if (blockIdx.x >= A.chunks) {                                  // queries: one row a block
         const int64_t t = blockIdx.x - A.chunks;
-        const int b = seq_of_row(A.B, t);
-        if (b < 0) return;
-        const Seq s = seq_info(A.B, b, A.T);
-        const int64_t pos = s.start + (t - s.row0);
-        if (pos < 0 || pos >= end) return;
-        const float2 *row = A.r.table + pos * (A.r.rot >> 1);
         const TI *x = static_cast<const TI *>(A.q.data) + t * A.q.ld_tok;
         TO *y = static_cast<TO *>(const_cast<void *>(A.q_out.data)) + t * A.q_out.ld_tok;
-        const bool vec = A.r.interleaved ? A.r.rot % 8 == 0 : A.r.rot % 16 == 0;
-        const int per = vec ? rope_items(D, A.r.rot, A.r.interleaved) : D / 2;
-        for (int i = blockIdx.y * kAppendThreads + threadIdx.x; i < per * A.q.heads; i += gridDim.y * kAppendThreads) {
-            const int h = i / per, j = i - h * per;
-            if (vec) rope_item(x + h * A.q.ld_head, y + h * A.q_out.ld_head, row, A.r, 1.0f, j);
-            else rope_pair(x + h * A.q.ld_head, y + h * A.q_out.ld_head, row, A.r, 1.0f, j);
+        const int tid = blockIdx.y * kAppendThreads + threadIdx.x, threads = gridDim.y * kAppendThreads;
+        auto position = [&]() -> const float2 * {
+            const int b = seq_of_row(A.B, t);
+            if (b < 0) return nullptr;
+            const Seq s = seq_info(A.B, b, A.T);
+            const int64_t pos = s.start + (t - s.row0);
+            return pos < 0 || pos >= end ? nullptr : A.r.table + pos * (A.r.rot >> 1);
+        };
+        if (A.r.interleaved) {
+            if (A.r.rot % 8 == 0) rope_token<true, true>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
+            else rope_token<true, false>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
+        } else {
+            if (A.r.rot % 16 == 0) rope_token<false, true>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
+            else rope_token<false, false>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
         }
         return;
     }
     // the chunk's rows: lane i looks at row chunk0 + i (every warp does the same)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x * (int64_t)A.chunk + lane;
+    const int64_t row = blockIdx.x * (int64_t)CHUNK + lane;
     int b = -1;
-    int64_t pos = 0;
-    Seq s = {};
+    int64_t pos = 0, len = 0;
     bool lead = false;
-    if (lane < A.chunk && row < A.T) {
+    if (lane < CHUNK && row < A.T) {
         b = seq_of_row(A.B, row);
         if (b >= 0) {
-            s = seq_info(A.B, b, A.T);
+            const Seq s = seq_info(A.B, b, A.T);
+            len = s.len;
             pos = s.start + (row - s.row0);
             const int64_t first = s.start > 0 ? s.start : 0;
             lead = pos >= first && pos < end && (pos == first || pos % kBlock == 0);
@@ -470,17 +542,16 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
         }
     }
     const unsigned leads = __ballot_sync(0xffffffffu, lead);
-    const int per = 2 * A.C.heads, items = __popc(leads) * per;
-    const int warps = kAppendThreads / 32;
-    for (int it = blockIdx.y * warps + warp; it < items; it += gridDim.y * warps) {
+    const int per = 2 * A.C.heads, items = __popc(leads) * per, team = warp / TEAM;
+    int turn = 0;
+    for (int it = blockIdx.y * TEAMS + team; it < items; it += gridDim.y * TEAMS, turn ^= 1) {
         const int k = it / per, hv = it - k * per;
-        const int src = __fns(leads, 0, k + 1);                    // the lane of leader k
-        Seq ss;
-        ss.len = __shfl_sync(0xffffffffu, s.len, src);
-        const int bb = __shfl_sync(0xffffffffu, b, src);
-        const int64_t pp = __shfl_sync(0xffffffffu, pos, src);
-        const int64_t rr = __shfl_sync(0xffffffffu, row, src);
-        append_block<TI, D>(A, ss, bb, pp, rr, hv >> 1, hv & 1);
+        unsigned rest = leads;
+        for (int i = 0; i < k; ++i) rest &= rest - 1;
+        const int src = __ffs(rest) - 1;                           // the lane of leader k
+        append_block<TI, D, TEAM>(A, __shfl_sync(0xffffffffu, len, src), __shfl_sync(0xffffffffu, b, src),
+                                  __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, row, src), hv >> 1, hv & 1,
+                                  warp % TEAM, team, share[team][turn]);
     }
 }
 

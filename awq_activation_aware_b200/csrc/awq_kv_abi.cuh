@@ -67,48 +67,6 @@ awq::kv::Rope kv_rope(const awq_rope_cfg &r) {
     return {reinterpret_cast<const float2 *>(r.table), r.n_pos, r.rot_dim, r.layout == AWQ_ROPE_INTERLEAVED};
 }
 
-template <typename TI, typename TO>
-void launch_rope(const awq::kv::RopeArgs &A, int64_t T, bool vec, cudaStream_t st) {
-    const int64_t items = (int64_t)A.x.heads * (vec ? awq::kv::rope_items(A.dim, A.r.rot, A.r.interleaved) : A.dim / 2);
-    const int threads = items >= 256 ? 256 : (int)((items + 31) / 32 * 32);
-    if (vec) awq::kv::rope_kernel<TI, TO, true><<<(unsigned)T, threads, 0, st>>>(A);
-    else awq::kv::rope_kernel<TI, TO, false><<<(unsigned)T, threads, 0, st>>>(A);
-}
-template <typename TI>
-void launch_rope_to(const awq::kv::RopeArgs &A, int64_t T, bool vec, cudaStream_t st) {
-    if (A.y.dtype == awq::kv::kF32) launch_rope<TI, float>(A, T, vec, st);
-    else if (A.y.dtype == awq::kv::kF16) launch_rope<TI, __half>(A, T, vec, st);
-    else launch_rope<TI, __nv_bfloat16>(A, T, vec, st);
-}
-
-template <typename TI, typename TO>
-void launch_append_dim(const awq::kv::AppendArgs &A, dim3 grid, cudaStream_t st) {
-    if (A.C.dim == 64) awq::kv::kv_append_kernel<TI, TO, 64><<<grid, awq::kv::kAppendThreads, 0, st>>>(A);
-    else awq::kv::kv_append_kernel<TI, TO, 128><<<grid, awq::kv::kAppendThreads, 0, st>>>(A);
-}
-template <typename TI>
-void launch_append(const awq::kv::AppendArgs &A, dim3 grid, cudaStream_t st) {
-    if (A.q_out.dtype == awq::kv::kF32) launch_append_dim<TI, float>(A, grid, st);
-    else if (A.q_out.dtype == awq::kv::kF16) launch_append_dim<TI, __half>(A, grid, st);
-    else launch_append_dim<TI, __nv_bfloat16>(A, grid, st);
-}
-
-// Codes as a 2-D tensor of bytes [n_pages * heads * page][D], boxes of `box_rows`
-// rows, swizzled over their width or as they are.
-bool encode_kv_map(CUtensorMap *m, const void *codes, const awq::kv::Cache &c, int box_rows, bool swizzle = true) {
-    EncodeTiledFn fn = encode_fn();
-    if (!fn) return false;
-    cuuint64_t dims[2] = {(cuuint64_t)c.dim, (cuuint64_t)(c.n_pages * c.heads * c.page)};
-    cuuint64_t strides[1] = {(cuuint64_t)c.dim};
-    cuuint32_t box[2] = {(cuuint32_t)c.dim, (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE,
-              !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
-                       : (c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B),
-              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // A launch whose start may overlap the end of the kernel before it on the stream
 // (programmatic dependent launch): the kernel waits for that one (griddep_wait)
 // before it reads or writes anything in global memory, in every block of threads.
@@ -125,6 +83,50 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_rope(const awq::kv::RopeArgs &A, int64_t T, bool vec, cudaStream_t st) {
+    const int64_t items = (int64_t)A.x.heads * (vec ? awq::kv::rope_items(A.dim, A.r.rot, A.r.interleaved) : A.dim / 2);
+    const int threads = items >= 256 ? 256 : (int)((items + 31) / 32 * 32);
+    auto kernel = A.r.interleaved ? (vec ? awq::kv::rope_kernel<TI, TO, true, true> : awq::kv::rope_kernel<TI, TO, true, false>)
+                                  : (vec ? awq::kv::rope_kernel<TI, TO, false, true> : awq::kv::rope_kernel<TI, TO, false, false>);
+    return launch_overlapped(kernel, dim3((unsigned)T), threads, 0, st, A);
+}
+template <typename TI>
+cudaError_t launch_rope_to(const awq::kv::RopeArgs &A, int64_t T, bool vec, cudaStream_t st) {
+    if (A.y.dtype == awq::kv::kF32) return launch_rope<TI, float>(A, T, vec, st);
+    if (A.y.dtype == awq::kv::kF16) return launch_rope<TI, __half>(A, T, vec, st);
+    return launch_rope<TI, __nv_bfloat16>(A, T, vec, st);
+}
+
+template <typename TI, typename TO>
+cudaError_t launch_append_dim(const awq::kv::AppendArgs &A, dim3 grid, cudaStream_t st) {
+    auto kernel = A.B.cu ? (A.C.dim == 64 ? awq::kv::kv_append_kernel<TI, TO, 64, 4> : awq::kv::kv_append_kernel<TI, TO, 128, 4>)
+                         : (A.C.dim == 64 ? awq::kv::kv_append_kernel<TI, TO, 64, 1> : awq::kv::kv_append_kernel<TI, TO, 128, 1>);
+    return launch_overlapped(kernel, grid, awq::kv::kAppendThreads, 0, st, A);
+}
+template <typename TI>
+cudaError_t launch_append(const awq::kv::AppendArgs &A, dim3 grid, cudaStream_t st) {
+    if (A.q_out.dtype == awq::kv::kF32) return launch_append_dim<TI, float>(A, grid, st);
+    if (A.q_out.dtype == awq::kv::kF16) return launch_append_dim<TI, __half>(A, grid, st);
+    return launch_append_dim<TI, __nv_bfloat16>(A, grid, st);
+}
+
+// Codes as a 2-D tensor of bytes [n_pages * heads * page][D], boxes of `box_rows`
+// rows, swizzled over their width or as they are.
+bool encode_kv_map(CUtensorMap *m, const void *codes, const awq::kv::Cache &c, int box_rows, bool swizzle = true) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)c.dim, (cuuint64_t)(c.n_pages * c.heads * c.page)};
+    cuuint64_t strides[1] = {(cuuint64_t)c.dim};
+    cuuint32_t box[2] = {(cuuint32_t)c.dim, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(codes), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
+                       : (c.dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B),
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Runs `set` the first time it is reached on the current device (one flag per use of a lambda type).
@@ -312,10 +314,10 @@ awq_status awq_rope(awq_rows x, awq_rows y, int64_t T, int32_t head_dim, const i
     const bool vec = kv_rows_aligned(x) && kv_rows_aligned(y) && head_dim % 8 == 0 &&
                      r.rot_dim % (A.r.interleaved ? 8 : 16) == 0;
     cudaStream_t st = (cudaStream_t)stream;
-    if (x.dtype == AWQ_F32) launch_rope_to<float>(A, T, vec, st);
-    else if (x.dtype == AWQ_F16) launch_rope_to<__half>(A, T, vec, st);
-    else launch_rope_to<__nv_bfloat16>(A, T, vec, st);
-    return last_launch();
+    cudaError_t e = x.dtype == AWQ_F32   ? launch_rope_to<float>(A, T, vec, st)
+                    : x.dtype == AWQ_F16 ? launch_rope_to<__half>(A, T, vec, st)
+                                         : launch_rope_to<__nv_bfloat16>(A, T, vec, st);
+    return cuda_status(e);
 }
 
 awq_status awq_kv_append(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows k, awq_rows v, awq_rows q, awq_rows q_out,
@@ -344,19 +346,20 @@ awq_status awq_kv_append(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows k, 
     A.q = kv_rows(q);
     A.q_out = kv_rows(q.data ? q_out : k);
     A.r = r.table ? kv_rope(r) : awq::kv::Rope{nullptr, 0, 0, 0};
-    A.chunk = b.cu_tokens ? 16 : 1;
-    A.chunks = (T + A.chunk - 1) / A.chunk;
+    const int chunk = b.cu_tokens ? 16 : 1, teams = awq::kv::kAppendThreads / 32 / (b.cu_tokens ? 4 : 1);
+    A.chunks = (T + chunk - 1) / chunk;
     const int64_t blocks = A.chunks + (q.data ? T : 0);
     if (blocks > kMaxDim) return AWQ_ERR_INVALID_ARG;
-    // several blocks share a chunk while the machine is not full
-    int gy = 1;
-    while (gy * 2 * 8 <= 2 * c.heads * A.chunk && blocks * gy < 4 * d.sms) gy *= 2;
+    // a team takes about one (block, head, keys or values) while that does not make far too many blocks of threads
+    const int items = 2 * c.heads;
+    int64_t gy = (items + teams - 1) / teams;
+    while (gy > 1 && blocks * gy > 64 * d.sms) gy = (gy + 1) / 2;
     const dim3 grid((unsigned)blocks, (unsigned)gy);
     cudaStream_t st = (cudaStream_t)stream;
-    if (k.dtype == AWQ_F32) launch_append<float>(A, grid, st);
-    else if (k.dtype == AWQ_F16) launch_append<__half>(A, grid, st);
-    else launch_append<__nv_bfloat16>(A, grid, st);
-    return last_launch();
+    cudaError_t e = k.dtype == AWQ_F32   ? launch_append<float>(A, grid, st)
+                    : k.dtype == AWQ_F16 ? launch_append<__half>(A, grid, st)
+                                         : launch_append<__nv_bfloat16>(A, grid, st);
+    return cuda_status(e);
 }
 
 size_t awq_kv_attention_workspace_bytes(awq_kv_cache c, int64_t T, int32_t q_heads, int32_t max_tokens) {
