@@ -221,6 +221,7 @@ __device__ __forceinline__ float2 rotate(float x1, float x2, float2 cs) {
 // ---------------------------------------------------------------------------
 struct RopeArgs {
     Rows x, y;
+    int64_t T;
     int dim, inverse;
     const int32_t *positions;
     Rope r;
@@ -270,7 +271,7 @@ __device__ __forceinline__ void rope_token(const TI *x, int64_t ldx, TO *y, int6
     const int wide = per < threads ? per : threads, step = threads / wide, h0 = tid / wide;
     if (h0 >= step) return;
     if constexpr (VEC) {
-        constexpr int U = 2;                                       // heads on their way at a time
+        constexpr int U = INTER ? 4 : 2;                           // heads on their way at a time: 32 elements
         const float2 *row = nullptr;
         for (int j = tid % wide; j < per; j += wide) {
             const bool turn = (INTER ? 8 : 16) * j < r.rot;
@@ -324,18 +325,21 @@ __device__ __forceinline__ void rope_token(const TI *x, int64_t ldx, TO *y, int6
     }
 }
 template <typename TI, typename TO, bool INTER, bool VEC>
-__global__ void __launch_bounds__(256, 4) rope_kernel(const RopeArgs A) {
+__global__ void __launch_bounds__(128, 8) rope_kernel(const RopeArgs A) {
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t t = blockIdx.x;
-    rope_token<INTER, VEC>(static_cast<const TI *>(A.x.data) + t * A.x.ld_tok, A.x.ld_head,
-                           static_cast<TO *>(const_cast<void *>(A.y.data)) + t * A.y.ld_tok, A.y.ld_head, A.r,
-                           A.inverse ? -1.0f : 1.0f, A.dim, A.x.heads, threadIdx.x, blockDim.x, [&]() -> const float2 * {
-                               const int64_t pos = A.positions[t];
-                               if (pos >= 0 && pos < A.r.n_pos) return A.r.table + pos * (A.r.rot >> 1);
-                               atomicOr(&g_dev_error, kDevErrBadIndex);
-                               return nullptr;
-                           });
+    int64_t next = A.positions[blockIdx.x];
+    for (int64_t t = blockIdx.x; t < A.T; t += gridDim.x) {
+        const int64_t pos = next;
+        if (t + gridDim.x < A.T) next = A.positions[t + gridDim.x];
+        rope_token<INTER, VEC>(static_cast<const TI *>(A.x.data) + t * A.x.ld_tok, A.x.ld_head,
+                               static_cast<TO *>(const_cast<void *>(A.y.data)) + t * A.y.ld_tok, A.y.ld_head, A.r,
+                               A.inverse ? -1.0f : 1.0f, A.dim, A.x.heads, threadIdx.x, blockDim.x, [&]() -> const float2 * {
+                                   if (pos >= 0 && pos < A.r.n_pos) return A.r.table + pos * (A.r.rot >> 1);
+                                   atomicOr(&g_dev_error, kDevErrBadIndex);
+                                   return nullptr;
+                               });
+    }
 }
 
 // ---------------------------------------------------------------------------

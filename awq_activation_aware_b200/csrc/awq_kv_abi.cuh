@@ -86,18 +86,21 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
 }
 
 template <typename TI, typename TO>
-cudaError_t launch_rope(const awq::kv::RopeArgs &A, int64_t T, bool vec, cudaStream_t st) {
+cudaError_t launch_rope(const awq::kv::RopeArgs &A, int64_t T, bool vec, int sms, cudaStream_t st) {
     const int64_t items = (int64_t)A.x.heads * (vec ? awq::kv::rope_items(A.dim, A.r.rot, A.r.interleaved) : A.dim / 2);
-    const int threads = items >= 256 ? 256 : (int)((items + 31) / 32 * 32);
+    // enough threads for one round of loads a token, blocks for 1024 threads an SM
+    const int64_t want = (items / (A.r.interleaved ? 4 : 2) + 31) / 32 * 32;
+    const int threads = want < 32 ? 32 : (want > 128 ? 128 : (int)want);
+    const int64_t grid = std::min<int64_t>(T, (int64_t)sms * (1024 / threads));
     auto kernel = A.r.interleaved ? (vec ? awq::kv::rope_kernel<TI, TO, true, true> : awq::kv::rope_kernel<TI, TO, true, false>)
                                   : (vec ? awq::kv::rope_kernel<TI, TO, false, true> : awq::kv::rope_kernel<TI, TO, false, false>);
-    return launch_overlapped(kernel, dim3((unsigned)T), threads, 0, st, A);
+    return launch_overlapped(kernel, dim3((unsigned)grid), threads, 0, st, A);
 }
 template <typename TI>
-cudaError_t launch_rope_to(const awq::kv::RopeArgs &A, int64_t T, bool vec, cudaStream_t st) {
-    if (A.y.dtype == awq::kv::kF32) return launch_rope<TI, float>(A, T, vec, st);
-    if (A.y.dtype == awq::kv::kF16) return launch_rope<TI, __half>(A, T, vec, st);
-    return launch_rope<TI, __nv_bfloat16>(A, T, vec, st);
+cudaError_t launch_rope_to(const awq::kv::RopeArgs &A, int64_t T, bool vec, int sms, cudaStream_t st) {
+    if (A.y.dtype == awq::kv::kF32) return launch_rope<TI, float>(A, T, vec, sms, st);
+    if (A.y.dtype == awq::kv::kF16) return launch_rope<TI, __half>(A, T, vec, sms, st);
+    return launch_rope<TI, __nv_bfloat16>(A, T, vec, sms, st);
 }
 
 template <typename TI, typename TO>
@@ -305,6 +308,7 @@ awq_status awq_rope(awq_rows x, awq_rows y, int64_t T, int32_t head_dim, const i
     DevInfo d;
     if (awq_status e = device_info(d)) return e;
     awq::kv::RopeArgs A;
+    A.T = T;
     A.x = kv_rows(x);
     A.y = kv_rows(y);
     A.dim = head_dim;
@@ -314,9 +318,9 @@ awq_status awq_rope(awq_rows x, awq_rows y, int64_t T, int32_t head_dim, const i
     const bool vec = kv_rows_aligned(x) && kv_rows_aligned(y) && head_dim % 8 == 0 &&
                      r.rot_dim % (A.r.interleaved ? 8 : 16) == 0;
     cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = x.dtype == AWQ_F32   ? launch_rope_to<float>(A, T, vec, st)
-                    : x.dtype == AWQ_F16 ? launch_rope_to<__half>(A, T, vec, st)
-                                         : launch_rope_to<__nv_bfloat16>(A, T, vec, st);
+    cudaError_t e = x.dtype == AWQ_F32   ? launch_rope_to<float>(A, T, vec, d.sms, st)
+                    : x.dtype == AWQ_F16 ? launch_rope_to<__half>(A, T, vec, d.sms, st)
+                                         : launch_rope_to<__nv_bfloat16>(A, T, vec, d.sms, st);
     return cuda_status(e);
 }
 
