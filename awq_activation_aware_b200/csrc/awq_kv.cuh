@@ -343,14 +343,14 @@ __global__ void __launch_bounds__(128, 8) rope_kernel(const RopeArgs A) {
 }
 
 // ---------------------------------------------------------------------------
-// Append.  A team of warps per (block of 16 positions that gets new tokens, head, keys or
-// values): four warps of four rows each, whose values stay in registers, so k and v are
-// read once, the block's exponent is known before any code is written, and no two teams
+// Append.  A team of warps per (block of 16 positions that gets new tokens, head): four
+// warps of four rows of keys and values each, which stay in registers, so k and v are
+// read once, the block's exponents are known before any code is written, and no two teams
 // touch the same block; one warp and one row where every sequence has one new token.
 // Bound by the bytes of k, v and q; in decode by latency.
 // Rows are dealt to blocks of threads in chunks: the rows of a chunk that open a
-// block (its leaders) are found by a ballot, and (leader, head, k / v) items go
-// round the teams.  A second range of the grid rotates the queries.
+// block (its leaders) are found by a ballot, and (leader, head) items go round the teams.
+// Other blocks of threads of the same launch rotate the queries.
 // ---------------------------------------------------------------------------
 struct AppendArgs {
     Cache C;
@@ -358,7 +358,9 @@ struct AppendArgs {
     int64_t T;
     Rows kv[2], q, q_out;
     Rope r;                    // table NULL: no rotation
-    int64_t chunks;            // blocks in x that append; those past them rotate queries
+    int64_t appends;           // blocks of threads that append: `parts` for a chunk of rows
+    int parts;
+    int q_rows;                // rows of queries of each of the others, at most 32
 };
 constexpr int kAppendThreads = 256;
 
@@ -367,49 +369,19 @@ __device__ __forceinline__ int64_t last_position(const Batch &B, const Cache &C,
     if (r.table && r.n_pos < end) end = r.n_pos;
     return end;
 }
-// Elements [d0, d0 + N) of the rotated row (N = D / 32 a lane).
+// Elements [d0, d0 + N) of a row, v, rotated one by one: for tables whose pairs do not lie side by side in a lane.
 template <typename TI, int N>
-__device__ __forceinline__ void rotated(const TI *x, const float2 *row, const Rope &r, int d0, float (&v)[N]) {
-    load_n(x + d0, v);
-    if (!row || d0 >= r.rot) return;
+__device__ __forceinline__ void rotate_apart(const TI *x, const float2 *row, const Rope &r, int d0, float (&v)[N]) {
     const int half = r.rot >> 1;
-    if (r.interleaved) {
-        if (N == 4 && half % 2 == 0 && d0 + N <= r.rot) {          // two pairs: one 16-byte load of the table
-            float2 cs[2];
-            load_cs(row + (d0 >> 1), 1.0f, cs);
 #pragma unroll
-            for (int j = 0; j < N; j += 2) {
-                const float2 z = rotate(v[j], v[j + 1], cs[j / 2]);
-                v[j] = z.x;
-                v[j + 1] = z.y;
-            }
-            return;
-        }
-#pragma unroll
-        for (int j = 0; j < N; j += 2) {
-            if (d0 + j >= r.rot) continue;
-            const float2 z = rotate(v[j], v[j + 1], row[(d0 + j) >> 1]);
-            v[j] = z.x;
-            v[j + 1] = z.y;
-        }
-    } else if (half % N == 0 && half % 2 == 0) {                   // the lane's elements have N neighbouring partners
-        const bool hi = d0 >= half;
-        float o[N];
-        float2 cs[N];
-        load_n(x + (hi ? d0 - half : d0 + half), o);
-        load_cs(row + (hi ? d0 - half : d0), 1.0f, cs);
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = hi ? rotate(o[j], v[j], cs[j]).y : rotate(v[j], o[j], cs[j]).x;
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int d = d0 + j;
-            if (d >= r.rot) continue;
-            const bool hi = d >= half;
-            const float other = to_f(x[hi ? d - half : d + half]);
-            const float2 cs = row[hi ? d - half : d];
-            v[j] = hi ? rotate(other, v[j], cs).y : rotate(v[j], other, cs).x;
-        }
+    for (int j = 0; j < N; ++j) {
+        const int d = d0 + j;
+        if (d >= r.rot) continue;
+        const bool hi = r.interleaved ? d & 1 : d >= half;
+        const int other = r.interleaved ? d ^ 1 : (hi ? d - half : d + half);
+        const float o = to_f(x[other]);
+        const float2 cs = row[r.interleaved ? d >> 1 : (hi ? d - half : d)];
+        v[j] = hi ? rotate(o, v[j], cs).y : rotate(v[j], o, cs).x;
     }
 }
 __device__ __forceinline__ uint16_t e4m3x2(float a, float b) {     // a in the low byte
@@ -433,109 +405,170 @@ __device__ __forceinline__ void store_codes(uint8_t *p, const float (&v)[N], flo
     else *reinterpret_cast<uint16_t *>(p) = w[0];
 }
 
-// One item.  TEAM warps (this is number `member`) with kBlock / TEAM rows each, or one with one row.
-template <typename TI, int D, int TEAM>
-__device__ __forceinline__ void append_block(const AppendArgs &A, int64_t len, int b, int64_t pos, int64_t row, int head,
-                                             int which, int member, int team, float *share) {
+// One item: keys and values of one head and block.  TEAM warps (this is number `member`) with kBlock / TEAM rows
+// each, or one with one row.  `page` is the block's, `share` [2][4].
+template <typename TI, int D, int TEAM, bool INTER>
+__device__ __forceinline__ void append_block(const AppendArgs &A, int64_t len, int64_t end, int64_t page, int64_t pos,
+                                             int64_t row, int head, int member, int team, float *share) {
     constexpr int N = D / 32, OWN = TEAM == 1 ? 1 : kBlock / TEAM;
-    const int lane = threadIdx.x & 31, d0 = lane * N;
-    const int64_t end = last_position(A.B, A.C, A.r);
+    const int lane = threadIdx.x & 31, d0 = lane * N, k0 = member * OWN;
     const int off = (int)(pos % kBlock);                           // rows of the block from before
-    const int64_t page = page_of(A.B, A.C, b, pos);                // the same for the whole team
-    if (page < 0) return;
     int n = kBlock - off;
     if (len - pos < n) n = (int)(len - pos);
     if (end - pos < n) n = (int)(end - pos);
-    const Rows &R = A.kv[which];
-    const TI *x = static_cast<const TI *>(R.data) + row * R.ld_tok + head * R.ld_head;
-    const int half = A.r.rot >> 1;
-    const bool turn = which == 0 && A.r.table != nullptr;
     const int64_t tile = (page * A.C.heads + head) * A.C.page + pos % A.C.page;     // first row written
-    float *scale = A.C.scales[which] + tile / kBlock;
-    uint8_t *codes = A.C.codes[which] + tile * D + d0;
-    const int e_old = off ? exponent_of(*scale) : kEMin;
-    float v[OWN][N];
-    float amax = 0.0f;
+    const TI *x[2];
 #pragma unroll
-    for (int i = 0; i < OWN; ++i) {
-        const int k = member * OWN + i;
-        if (k < n) rotated<TI, N>(x + k * R.ld_tok, turn ? A.r.table + (pos + k) * half : nullptr, A.r, d0, v[i]);
-    }
+    for (int w = 0; w < 2; ++w)
+        x[w] = static_cast<const TI *>(A.kv[w].data) + (row + k0) * A.kv[w].ld_tok + head * A.kv[w].ld_head;
+    // all loads first: rows of values and keys, the keys' partners where they are neighbours (half layout), cosines and sines
+    const int half = A.r.rot >> 1, lo = INTER ? d0 >> 1 : (d0 < half ? d0 : d0 - half);
+    const bool near = INTER ? A.r.rot % N == 0 : half % N == 0 && half % 2 == 0, turn = A.r.table && d0 < A.r.rot;
+    const bool pair = !INTER && near && turn;
+    Raw<TI, N> rv[OWN], rk[OWN], ro[OWN];
 #pragma unroll
     for (int i = 0; i < OWN; ++i)
-        if (member * OWN + i < n) {
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (isfinite(v[i][j])) amax = fmaxf(amax, fabsf(v[i][j]));
+        if (k0 + i < n) {
+            rv[i].load(x[1] + i * A.kv[1].ld_tok + d0);
+            rk[i].load(x[0] + i * A.kv[0].ld_tok + d0);
+            if (pair) ro[i].load(x[0] + i * A.kv[0].ld_tok + (d0 < half ? d0 + half : d0 - half));
         }
-    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+    int e_old[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) e_old[w] = off ? exponent_of(A.C.scales[w][tile / kBlock]) : kEMin;
+    float v[2][OWN][N], amax[2] = {0.0f, 0.0f};
+    const float2 *table = A.r.table + (pos + k0) * half + lo;
+    if (near && turn) {
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            float2 cs[N];
+            if (k0 + i < n) {
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (!INTER || j < N / 2) cs[j] = table[i * half + j];
+            }
+            rk[i].take(v[0][i]);
+            if (INTER) {
+#pragma unroll
+                for (int j = 0; j < N; j += 2) {
+                    const float2 z = rotate(v[0][i][j], v[0][i][j + 1], cs[j / 2]);
+                    v[0][i][j] = z.x;
+                    v[0][i][j + 1] = z.y;
+                }
+            } else {
+                float o[N];
+                ro[i].take(o);
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    v[0][i][j] = d0 < half ? rotate(v[0][i][j], o[j], cs[j]).x : rotate(o[j], v[0][i][j], cs[j]).y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < OWN; ++i) {
+            rk[i].take(v[0][i]);
+            if (turn && k0 + i < n) rotate_apart<TI, N>(x[0] + i * A.kv[0].ld_tok, A.r.table + (pos + k0 + i) * half, A.r, d0, v[0][i]);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < OWN; ++i) {
+        rv[i].take(v[1][i]);
+        if (k0 + i < n) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+#pragma unroll
+                for (int j = 0; j < N; ++j)
+                    if (isfinite(v[w][i][j])) amax[w] = fmaxf(amax[w], fabsf(v[w][i][j]));
+        }
+    }
+#pragma unroll
+    for (int w = 0; w < 2; ++w) amax[w] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax[w])));
     if (TEAM > 1) {
-        if (lane == 0) share[member] = amax;
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * TEAM) : "memory");       // every warp has read the old scale, too
-        amax = fmaxf(fmaxf(share[0], share[1]), fmaxf(share[2], share[3]));
+        if (lane < 2) share[4 * lane + member] = lane ? amax[1] : amax[0];
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * TEAM) : "memory");       // every warp has read the old scales, too
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+            amax[w] = fmaxf(fmaxf(share[4 * w], share[4 * w + 1]), fmaxf(share[4 * w + 2], share[4 * w + 3]));
     } else {
         __syncwarp();
     }
-    int e = exponent_for(amax);
-    if (e > e_old) {
-        const float f = pow2(e_old - e);
-        for (int i = 1 + member; i <= off; i += TEAM) {            // the codes from before, in the new scale
-            uint8_t *p = codes - i * D;
-            uint16_t w[N / 2];
 #pragma unroll
-            for (int j = 0; j < N / 2; ++j) {
-                const float2 o = from_e4m3x2(reinterpret_cast<const uint16_t *>(p)[j]);
-                w[j] = e4m3x2(o.x * f, o.y * f);
+    for (int w = 0; w < 2; ++w) {
+        uint8_t *codes = A.C.codes[w] + tile * D + d0;
+        int e = exponent_for(amax[w]);
+        if (e > e_old[w]) {
+            const float f = pow2(e_old[w] - e);
+            for (int i = 1 + member; i <= off; i += TEAM) {        // the codes from before, in the new scale
+                uint8_t *p = codes - i * D;
+                uint16_t c[N / 2];
+#pragma unroll
+                for (int j = 0; j < N / 2; ++j) {
+                    const float2 o = from_e4m3x2(reinterpret_cast<const uint16_t *>(p)[j]);
+                    c[j] = e4m3x2(o.x * f, o.y * f);
+                }
+#pragma unroll
+                for (int j = 0; j < N / 2; ++j) reinterpret_cast<uint16_t *>(p)[j] = c[j];
             }
-#pragma unroll
-            for (int j = 0; j < N / 2; ++j) reinterpret_cast<uint16_t *>(p)[j] = w[j];
+        } else {
+            e = e_old[w];
         }
-    } else {
-        e = e_old;
-    }
-    if (lane == 0 && member == 0) *scale = pow2(e);
-    const float inv = pow2(-e);
+        if (lane == 0 && member == 0) A.C.scales[w][tile / kBlock] = pow2(e);
+        const float inv = pow2(-e);
 #pragma unroll
-    for (int i = 0; i < OWN; ++i)
-        if (member * OWN + i < n) store_codes<N>(codes + (member * OWN + i) * D, v[i], inv);
+        for (int i = 0; i < OWN; ++i)
+            if (k0 + i < n) store_codes<N>(codes + (k0 + i) * D, v[w][i], inv);
+    }
 }
 
-template <typename TI, typename TO, int D, int TEAM>
-__global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const AppendArgs A) {
+// Position of row t, -1 if it has none that the tables cover.
+__device__ __forceinline__ int64_t position_of(const AppendArgs &A, int64_t t, int64_t end) {
+    if (t >= A.T) return -1;
+    const int b = seq_of_row(A.B, t);
+    if (b < 0) return -1;
+    const Seq s = seq_info(A.B, b, A.T);
+    const int64_t pos = s.start + (t - s.row0);
+    return pos < end ? pos : -1;
+}
+
+template <typename TI, typename TO, int D, int TEAM, bool INTER>
+__global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const AppendArgs A) {
     constexpr int CHUNK = TEAM == 1 ? 1 : 16, WARPS = kAppendThreads / 32, TEAMS = WARPS / TEAM;
-    __shared__ float share[TEAMS][2][4];
+    __shared__ float share[TEAMS][2][8];
     griddep_launch_dependents();
     griddep_wait();
     const int64_t end = last_position(A.B, A.C, A.r);
-    if (blockIdx.x >= A.chunks) {                                  // queries: one row a block
-        const int64_t t = blockIdx.x - A.chunks;
-        const TI *x = static_cast<const TI *>(A.q.data) + t * A.q.ld_tok;
-        TO *y = static_cast<TO *>(const_cast<void *>(A.q_out.data)) + t * A.q_out.ld_tok;
-        const int tid = blockIdx.y * kAppendThreads + threadIdx.x, threads = gridDim.y * kAppendThreads;
-        auto position = [&]() -> const float2 * {
-            const int b = seq_of_row(A.B, t);
-            if (b < 0) return nullptr;
-            const Seq s = seq_info(A.B, b, A.T);
-            const int64_t pos = s.start + (t - s.row0);
-            return pos < 0 || pos >= end ? nullptr : A.r.table + pos * (A.r.rot >> 1);
-        };
-        if (A.r.interleaved) {
-            if (A.r.rot % 8 == 0) rope_token<true, true>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
-            else rope_token<true, false>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
-        } else {
-            if (A.r.rot % 16 == 0) rope_token<false, true>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
-            else rope_token<false, false>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
+    // the blocks that append lie evenly between those that rotate queries: the ones wait, the others stream
+    const int64_t before = blockIdx.x * A.appends / gridDim.x;
+    if (before == (blockIdx.x + 1) * A.appends / gridDim.x) {
+        // queries: the rows' positions are looked up by the lanes of every warp at once; a lone row takes all threads
+        const int lane = threadIdx.x & 31;
+        const int64_t row0 = (blockIdx.x - before) * A.q_rows;
+        const int64_t mine = lane < A.q_rows ? position_of(A, row0 + lane, end) : -1;
+        const int threads = A.q_rows == 1 ? kAppendThreads : kAppendThreads / 2;
+        const bool vec = A.r.rot % (INTER ? 8 : 16) == 0;
+        for (int i = threadIdx.x / threads; i < A.q_rows; i += kAppendThreads / threads) {
+            const int64_t pos = __shfl_sync(0xffffffffu, mine, i), t = row0 + i;
+            if (pos >= 0) {
+                const TI *x = static_cast<const TI *>(A.q.data) + t * A.q.ld_tok;
+                TO *y = static_cast<TO *>(const_cast<void *>(A.q_out.data)) + t * A.q_out.ld_tok;
+                auto position = [&]() -> const float2 * { return A.r.table + pos * (A.r.rot >> 1); };
+                const int tid = threadIdx.x % threads;
+                if (vec) rope_token<INTER, true>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
+                else rope_token<INTER, false>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
+            }
+            __syncwarp();
         }
         return;
     }
+    const int64_t at = before / A.parts;
     // the chunk's rows: lane i looks at row chunk0 + i (every warp does the same)
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x * (int64_t)CHUNK + lane;
-    int b = -1;
-    int64_t pos = 0, len = 0;
+    const int part = (int)(before % A.parts);
+    const int64_t row = at * CHUNK + lane;
+    int64_t pos = 0, len = 0, page = -1;
     bool lead = false;
     if (lane < CHUNK && row < A.T) {
-        b = seq_of_row(A.B, row);
+        const int b = seq_of_row(A.B, row);
         if (b >= 0) {
             const Seq s = seq_info(A.B, b, A.T);
             len = s.len;
@@ -543,18 +576,20 @@ __global__ void __launch_bounds__(kAppendThreads, 4) kv_append_kernel(const Appe
             const int64_t first = s.start > 0 ? s.start : 0;
             lead = pos >= first && pos < end && (pos == first || pos % kBlock == 0);
             if (pos >= end && threadIdx.x < 32) atomicOr(&g_dev_error, kDevErrBadIndex);
+            if (lead) page = page_of(A.B, A.C, b, pos);
+            lead = lead && page >= 0;
         }
     }
     const unsigned leads = __ballot_sync(0xffffffffu, lead);
-    const int per = 2 * A.C.heads, items = __popc(leads) * per, team = warp / TEAM;
+    const int items = __popc(leads) * A.C.heads, team = warp / TEAM;
     int turn = 0;
-    for (int it = blockIdx.y * TEAMS + team; it < items; it += gridDim.y * TEAMS, turn ^= 1) {
-        const int k = it / per, hv = it - k * per;
+    for (int it = part * TEAMS + team; it < items; it += A.parts * TEAMS, turn ^= 1) {
+        const int k = it / A.C.heads, head = it - k * A.C.heads;
         unsigned rest = leads;
         for (int i = 0; i < k; ++i) rest &= rest - 1;
         const int src = __ffs(rest) - 1;                           // the lane of leader k
-        append_block<TI, D, TEAM>(A, __shfl_sync(0xffffffffu, len, src), __shfl_sync(0xffffffffu, b, src),
-                                  __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, row, src), hv >> 1, hv & 1,
+        append_block<TI, D, TEAM, INTER>(A, __shfl_sync(0xffffffffu, len, src), end, __shfl_sync(0xffffffffu, page, src),
+                                  __shfl_sync(0xffffffffu, pos, src), __shfl_sync(0xffffffffu, row, src), head,
                                   warp % TEAM, team, share[team][turn]);
     }
 }

@@ -85,12 +85,16 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Threads of a block that rotates: enough for one round of loads a token; blocks of them make 1024 an SM.
+int rope_threads(int64_t items, bool interleaved) {
+    const int64_t want = (items / (interleaved ? 4 : 2) + 31) / 32 * 32;
+    return want < 32 ? 32 : (want > 128 ? 128 : (int)want);
+}
+
 template <typename TI, typename TO>
 cudaError_t launch_rope(const awq::kv::RopeArgs &A, int64_t T, bool vec, int sms, cudaStream_t st) {
     const int64_t items = (int64_t)A.x.heads * (vec ? awq::kv::rope_items(A.dim, A.r.rot, A.r.interleaved) : A.dim / 2);
-    // enough threads for one round of loads a token, blocks for 1024 threads an SM
-    const int64_t want = (items / (A.r.interleaved ? 4 : 2) + 31) / 32 * 32;
-    const int threads = want < 32 ? 32 : (want > 128 ? 128 : (int)want);
+    const int threads = rope_threads(items, A.r.interleaved);
     const int64_t grid = std::min<int64_t>(T, (int64_t)sms * (1024 / threads));
     auto kernel = A.r.interleaved ? (vec ? awq::kv::rope_kernel<TI, TO, true, true> : awq::kv::rope_kernel<TI, TO, true, false>)
                                   : (vec ? awq::kv::rope_kernel<TI, TO, false, true> : awq::kv::rope_kernel<TI, TO, false, false>);
@@ -103,10 +107,15 @@ cudaError_t launch_rope_to(const awq::kv::RopeArgs &A, int64_t T, bool vec, int 
     return launch_rope<TI, __nv_bfloat16>(A, T, vec, sms, st);
 }
 
+template <typename TI, typename TO, bool INTER>
+auto launch_append_of(int dim, bool ragged) {
+    return ragged ? (dim == 64 ? awq::kv::kv_append_kernel<TI, TO, 64, 4, INTER> : awq::kv::kv_append_kernel<TI, TO, 128, 4, INTER>)
+                  : (dim == 64 ? awq::kv::kv_append_kernel<TI, TO, 64, 1, INTER> : awq::kv::kv_append_kernel<TI, TO, 128, 1, INTER>);
+}
 template <typename TI, typename TO>
 cudaError_t launch_append_dim(const awq::kv::AppendArgs &A, dim3 grid, cudaStream_t st) {
-    auto kernel = A.B.cu ? (A.C.dim == 64 ? awq::kv::kv_append_kernel<TI, TO, 64, 4> : awq::kv::kv_append_kernel<TI, TO, 128, 4>)
-                         : (A.C.dim == 64 ? awq::kv::kv_append_kernel<TI, TO, 64, 1> : awq::kv::kv_append_kernel<TI, TO, 128, 1>);
+    const bool ragged = A.B.cu != nullptr;
+    auto kernel = A.r.interleaved ? launch_append_of<TI, TO, true>(A.C.dim, ragged) : launch_append_of<TI, TO, false>(A.C.dim, ragged);
     return launch_overlapped(kernel, grid, awq::kv::kAppendThreads, 0, st, A);
 }
 template <typename TI>
@@ -351,14 +360,15 @@ awq_status awq_kv_append(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows k, 
     A.q_out = kv_rows(q.data ? q_out : k);
     A.r = r.table ? kv_rope(r) : awq::kv::Rope{nullptr, 0, 0, 0};
     const int chunk = b.cu_tokens ? 16 : 1, teams = awq::kv::kAppendThreads / 32 / (b.cu_tokens ? 4 : 1);
-    A.chunks = (T + chunk - 1) / chunk;
-    const int64_t blocks = A.chunks + (q.data ? T : 0);
+    const int64_t chunks = (T + chunk - 1) / chunk;
+    // a team takes about one (block, head) while that does not make far too many blocks of threads
+    A.parts = (c.heads + teams - 1) / teams;
+    while (A.parts > 1 && chunks * A.parts > 16 * d.sms) A.parts = (A.parts + 1) / 2;
+    A.appends = chunks * A.parts;
+    A.q_rows = (int)std::min<int64_t>(8, std::max<int64_t>(1, T / (8 * d.sms)));
+    const int64_t blocks = A.appends + (q.data ? (T + A.q_rows - 1) / A.q_rows : 0);
     if (blocks > kMaxDim) return AWQ_ERR_INVALID_ARG;
-    // a team takes about one (block, head, keys or values) while that does not make far too many blocks of threads
-    const int items = 2 * c.heads;
-    int64_t gy = (items + teams - 1) / teams;
-    while (gy > 1 && blocks * gy > 64 * d.sms) gy = (gy + 1) / 2;
-    const dim3 grid((unsigned)blocks, (unsigned)gy);
+    const dim3 grid((unsigned)blocks);
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = k.dtype == AWQ_F32   ? launch_append<float>(A, grid, st)
                     : k.dtype == AWQ_F16 ? launch_append<__half>(A, grid, st)
