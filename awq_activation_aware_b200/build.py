@@ -16,9 +16,9 @@ PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
 CSRC = PKG / "csrc"
 LIB = PKG / "libawq.so"
-SOURCES = [CSRC / "awq_abi.cu"]
-DEPS = SOURCES + [CSRC / "awq_kernels.cuh", CSRC / "awq_device.cuh", CSRC / "awq_kv.cuh",
-                  CSRC / "awq_kv_decode.cuh", CSRC / "awq_kv_prefill.cuh", CSRC / "awq_kv_abi.cuh", ROOT / "include" / "awq.h"]
+SOURCES = [CSRC / "awq_abi.cu", CSRC / "awq_kv_abi.cu"]
+DEPS = SOURCES + [CSRC / n for n in ("awq_kernels.cuh", "awq_device.cuh", "awq_host.h", "awq_kv.cuh", "awq_kv_decode.cuh",
+                                     "awq_kv_prefill.cuh")] + [ROOT / "include" / "awq.h"]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",
@@ -26,9 +26,9 @@ NVCC_FLAGS = [
     "-lineinfo",
     "-fmad=false",          # no implicit multiply-add contraction: every FMA in the code is explicit
     "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
-    "-shared", "-cudart", "static",
     "-Xptxas", "-v",
 ]
+LINK_FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-cudart", "static"]
 
 
 def nvcc() -> str:
@@ -48,14 +48,27 @@ def build(force: bool = False, verbose: bool = False) -> Path:
     if not force and not needs_build():
         return LIB
     tmp = LIB.with_suffix(f".so.tmp{os.getpid()}")
-    cmd = [nvcc(), *NVCC_FLAGS, "-I", str(ROOT / "include"), "-I", str(CSRC),
-           "-o", str(tmp), *map(str, SOURCES)]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    log = res.stdout + res.stderr
-    (PKG / "build.log").write_text(" ".join(cmd) + "\n" + log)
-    if res.returncode != 0:
+    objs = [PKG / f"{src.stem}.tmp{os.getpid()}.o" for src in SOURCES]
+    cmds = [[nvcc(), *NVCC_FLAGS, "-I", str(ROOT / "include"), "-I", str(CSRC), "-c", "-o", str(obj), str(src)]
+            for src, obj in zip(SOURCES, objs)]
+    # the units compile side by side
+    procs = [subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for cmd in cmds]
+    log, code = "", 0
+    for cmd, proc in zip(cmds, procs):
+        out = proc.communicate()[0]
+        log += " ".join(cmd) + "\n" + out
+        code = code or proc.returncode
+    if code == 0:
+        cmd = [nvcc(), *LINK_FLAGS, "-o", str(tmp), *map(str, objs)]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        log += " ".join(cmd) + "\n" + res.stdout + res.stderr
+        code = res.returncode
+    for obj in objs:
+        obj.unlink(missing_ok=True)
+    (PKG / "build.log").write_text(log)
+    if code != 0:
         sys.stderr.write(log)
-        raise RuntimeError(f"nvcc failed ({res.returncode}); see {PKG / 'build.log'}")
+        raise RuntimeError(f"nvcc failed ({code}); see {PKG / 'build.log'}")
     if verbose:
         sys.stdout.write(log)
     os.replace(tmp, LIB)

@@ -7,16 +7,13 @@
 
 #include <algorithm>
 #include <atomic>
-#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
 
 #include "awq.h"
 #include "awq_kernels.cuh"
-#include "awq_kv.cuh"
-#include "awq_kv_decode.cuh"
-#include "awq_kv_prefill.cuh"
+#include "awq_host.h"
 
 namespace {
 
@@ -1001,17 +998,18 @@ awq_status awq_selftest_bounded_wait(void *stream) {
 awq_status awq_get_status(void *stream) {
     cudaError_t e = cudaStreamSynchronize((cudaStream_t)stream);
     if (e != cudaSuccess) return AWQ_ERR_CUDA;
-    unsigned flags = 0;
+    unsigned flags = 0, kv_bad = 0;
     if (cudaMemcpyFromSymbol(&flags, awq::g_dev_error, sizeof(flags)) != cudaSuccess) return AWQ_ERR_CUDA;
     if (flags) {
         const unsigned zero = 0;
         if (cudaMemcpyToSymbol(awq::g_dev_error, &zero, sizeof(zero)) != cudaSuccess) return AWQ_ERR_CUDA;
-        if (flags & awq::kDevErrTimeout) return AWQ_ERR_TIMEOUT;
-        if (flags & (awq::kDevErrBadAlpha | awq::kDevErrBadScale | awq::kDevErrNotPD | awq::kv::kDevErrBadIndex)) return AWQ_ERR_INVALID_ARG;
     }
+    if (!awq_host::take_kv_errors(&kv_bad)) return AWQ_ERR_CUDA;
+    if ((flags | kv_bad) & awq::kDevErrTimeout) return AWQ_ERR_TIMEOUT;
+    if (kv_bad || flags & (awq::kDevErrBadAlpha | awq::kDevErrBadScale | awq::kDevErrNotPD)) return AWQ_ERR_INVALID_ARG;
     return last_launch();
 }
 
 }  // extern "C"
 
-#include "awq_kv_abi.cuh"
+uint32_t awq_host::wait_timeout_ms() { return g_timeout_ms.load(); }

@@ -264,67 +264,80 @@ __device__ __forceinline__ void rope_place(const RX &ra, const RX &rb, TO *y, in
 }
 // All heads of one token, by `threads` threads of which this is number `tid`.  `position` is called once, after the
 // first heads' loads are out; it gives the table's row or NULL (nothing is written).
-template <bool INTER, bool VEC, typename TI, typename TO, typename POS>
+template <bool INTER, typename TI, typename TO, typename POS>
 __device__ __forceinline__ void rope_token(const TI *x, int64_t ldx, TO *y, int64_t ldy, const Rope &r, float sign, int dim,
                                            int heads, int tid, int threads, POS position) {
-    const int half = r.rot >> 1, per = VEC ? rope_items(dim, r.rot, INTER) : dim / 2;
+    const int half = r.rot >> 1, per = rope_items(dim, r.rot, INTER);
     const int wide = per < threads ? per : threads, step = threads / wide, h0 = tid / wide;
     if (h0 >= step) return;
-    if constexpr (VEC) {
-        constexpr int U = INTER ? 4 : 2;                           // heads on their way at a time: 32 elements
-        const float2 *row = nullptr;
-        for (int j = tid % wide; j < per; j += wide) {
-            const bool turn = (INTER ? 8 : 16) * j < r.rot;
-            const int d = INTER || turn ? 8 * j : r.rot + 8 * (j - (r.rot >> 4));
-            const bool two = !INTER && turn;
-            float2 cs[INTER ? 4 : 8];
-            for (int h = h0; h < heads; h += U * step) {
-                Raw<TI, 8> a[U], b[INTER ? 1 : U];
+    constexpr int U = INTER ? 4 : 2;                               // heads on their way at a time: 32 elements
+    const float2 *row = nullptr;
+    for (int j = tid % wide; j < per; j += wide) {
+        const bool turn = (INTER ? 8 : 16) * j < r.rot;
+        const int d = INTER || turn ? 8 * j : r.rot + 8 * (j - (r.rot >> 4));
+        const bool two = !INTER && turn;
+        float2 cs[INTER ? 4 : 8];
+        for (int h = h0; h < heads; h += U * step) {
+            Raw<TI, 8> a[U], b[INTER ? 1 : U];
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (h + u * step < heads) {
-                        a[u].load(x + (h + u * step) * ldx + d);
-                        if (two) b[INTER ? 0 : u].load(x + (h + u * step) * ldx + d + half);
-                    }
-                if (h == h0) {
-                    if (!row) row = position();
-                    if (!row) return;
-                    if (turn) load_cs(row + (INTER ? 4 : 8) * j, sign, cs);
+            for (int u = 0; u < U; ++u)
+                if (h + u * step < heads) {
+                    a[u].load(x + (h + u * step) * ldx + d);
+                    if (two) b[INTER ? 0 : u].load(x + (h + u * step) * ldx + d + half);
                 }
+            if (h == h0) {
+                if (!row) row = position();
+                if (!row) return;
+                if (turn) load_cs(row + (INTER ? 4 : 8) * j, sign, cs);
+            }
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (h + u * step < heads) {
-                        TO *to = y + (h + u * step) * ldy + d;
-                        if (!turn) rope_place<0>(a[u], a[u], to, half, cs);
-                        else if (INTER) rope_place<1>(a[u], a[u], to, half, cs);
-                        else rope_place<INTER ? 1 : 2>(a[u], b[INTER ? 0 : u], to, half, cs);
-                    }
-            }
-        }
-    } else {
-        const float2 *row = position();
-        if (!row) return;
-        for (int j = tid % wide; j < per; j += wide) {
-            int d1 = 2 * j, d2 = 2 * j + 1;
-            float2 cs = make_float2(1.0f, 0.0f);
-            if (j < half) {
-                cs = row[j];
-                cs.y *= sign;
-                if (!INTER) {
-                    d1 = j;
-                    d2 = j + half;
+            for (int u = 0; u < U; ++u)
+                if (h + u * step < heads) {
+                    TO *to = y + (h + u * step) * ldy + d;
+                    if (!turn) rope_place<0>(a[u], a[u], to, half, cs);
+                    else rope_place<INTER ? 1 : 2>(a[u], b[INTER ? 0 : u], to, half, cs);
                 }
-            }
-            for (int h = h0; h < heads; h += step) {
-                float2 z = make_float2(to_f(x[h * ldx + d1]), to_f(x[h * ldx + d2]));
-                if (j < half) z = rotate(z.x, z.y, cs);
-                y[h * ldy + d1] = from_f<TO>(z.x);
-                y[h * ldy + d2] = from_f<TO>(z.y);
-            }
         }
     }
 }
-template <typename TI, typename TO, bool INTER, bool VEC>
+// The same a pair at a time, for rows of any alignment, head_dim and rot; types and layout looked at as it goes.
+__device__ __forceinline__ float load_any(const void *p, int dtype, int64_t i) {
+    return dtype == kF32   ? static_cast<const float *>(p)[i]
+           : dtype == kF16 ? __half2float(static_cast<const __half *>(p)[i])
+                           : __bfloat162float(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+__device__ __forceinline__ void store_any(void *p, int dtype, int64_t i, float v) {
+    if (dtype == kF32) static_cast<float *>(p)[i] = v;
+    else if (dtype == kF16) static_cast<__half *>(p)[i] = __float2half_rn(v);
+    else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+__device__ __noinline__ void rope_token_any(const Rows x, const Rows y, int64_t t, const Rope r, const float2 *row, float sign,
+                                            int dim, int tid, int threads) {
+    const int half = r.rot >> 1;
+    for (int i = tid; i < dim / 2 * x.heads; i += threads) {
+        const int h = i / (dim / 2), j = i - h * (dim / 2);
+        const bool apart = j < half && !r.interleaved;
+        const int d1 = apart ? j : 2 * j, d2 = apart ? j + half : 2 * j + 1;
+        const int64_t from = t * x.ld_tok + h * x.ld_head, to = t * y.ld_tok + h * y.ld_head;
+        float2 z = make_float2(load_any(x.data, x.dtype, from + d1), load_any(x.data, x.dtype, from + d2));
+        if (j < half) z = rotate(z.x, z.y, make_float2(row[j].x, row[j].y * sign));
+        store_any(const_cast<void *>(y.data), y.dtype, to + d1, z.x);
+        store_any(const_cast<void *>(y.data), y.dtype, to + d2, z.y);
+    }
+}
+__device__ __forceinline__ const float2 *rope_row(const RopeArgs &A, int64_t pos) {
+    if (pos >= 0 && pos < A.r.n_pos) return A.r.table + pos * (A.r.rot >> 1);
+    atomicOr(&g_dev_error, kDevErrBadIndex);
+    return nullptr;
+}
+__global__ void __launch_bounds__(128, 8) rope_any_kernel(const RopeArgs A) {
+    griddep_launch_dependents();
+    griddep_wait();
+    for (int64_t t = blockIdx.x; t < A.T; t += gridDim.x)
+        if (const float2 *row = rope_row(A, A.positions[t]))
+            rope_token_any(A.x, A.y, t, A.r, row, A.inverse ? -1.0f : 1.0f, A.dim, threadIdx.x, blockDim.x);
+}
+template <typename TI, typename TO, bool INTER>
 __global__ void __launch_bounds__(128, 8) rope_kernel(const RopeArgs A) {
     griddep_launch_dependents();
     griddep_wait();
@@ -332,13 +345,10 @@ __global__ void __launch_bounds__(128, 8) rope_kernel(const RopeArgs A) {
     for (int64_t t = blockIdx.x; t < A.T; t += gridDim.x) {
         const int64_t pos = next;
         if (t + gridDim.x < A.T) next = A.positions[t + gridDim.x];
-        rope_token<INTER, VEC>(static_cast<const TI *>(A.x.data) + t * A.x.ld_tok, A.x.ld_head,
-                               static_cast<TO *>(const_cast<void *>(A.y.data)) + t * A.y.ld_tok, A.y.ld_head, A.r,
-                               A.inverse ? -1.0f : 1.0f, A.dim, A.x.heads, threadIdx.x, blockDim.x, [&]() -> const float2 * {
-                                   if (pos >= 0 && pos < A.r.n_pos) return A.r.table + pos * (A.r.rot >> 1);
-                                   atomicOr(&g_dev_error, kDevErrBadIndex);
-                                   return nullptr;
-                               });
+        rope_token<INTER>(static_cast<const TI *>(A.x.data) + t * A.x.ld_tok, A.x.ld_head,
+                          static_cast<TO *>(const_cast<void *>(A.y.data)) + t * A.y.ld_tok, A.y.ld_head, A.r,
+                          A.inverse ? -1.0f : 1.0f, A.dim, A.x.heads, threadIdx.x, blockDim.x,
+                          [&]() -> const float2 * { return rope_row(A, pos); });
     }
 }
 
@@ -549,12 +559,14 @@ __global__ void __launch_bounds__(kAppendThreads, 3) kv_append_kernel(const Appe
         for (int i = threadIdx.x / threads; i < A.q_rows; i += kAppendThreads / threads) {
             const int64_t pos = __shfl_sync(0xffffffffu, mine, i), t = row0 + i;
             if (pos >= 0) {
-                const TI *x = static_cast<const TI *>(A.q.data) + t * A.q.ld_tok;
-                TO *y = static_cast<TO *>(const_cast<void *>(A.q_out.data)) + t * A.q_out.ld_tok;
-                auto position = [&]() -> const float2 * { return A.r.table + pos * (A.r.rot >> 1); };
+                const float2 *table = A.r.table + pos * (A.r.rot >> 1);
                 const int tid = threadIdx.x % threads;
-                if (vec) rope_token<INTER, true>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
-                else rope_token<INTER, false>(x, A.q.ld_head, y, A.q_out.ld_head, A.r, 1.0f, D, A.q.heads, tid, threads, position);
+                if (vec)
+                    rope_token<INTER>(static_cast<const TI *>(A.q.data) + t * A.q.ld_tok, A.q.ld_head,
+                                      static_cast<TO *>(const_cast<void *>(A.q_out.data)) + t * A.q_out.ld_tok, A.q_out.ld_head,
+                                      A.r, 1.0f, D, A.q.heads, tid, threads, [&]() { return table; });
+                else
+                    rope_token_any(A.q, A.q_out, t, A.r, table, 1.0f, D, tid, threads);
             }
             __syncwarp();
         }

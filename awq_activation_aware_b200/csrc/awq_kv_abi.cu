@@ -1,8 +1,68 @@
 // Host side of the cache operators of include/awq.h: argument checks, workspace
-// layout and launches.  Included by awq_abi.cu after its helpers.
-#pragma once
+// layout and launches.  A translation unit of its own, so that both compile at
+// once; it has its own device error word, which awq_get_status() reads too.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+
+#include "awq.h"
+#include "awq_host.h"
+
+#define g_dev_error g_kv_dev_error             // this unit's word, defined with the helpers of awq_device.cuh
+#include "awq_kv.cuh"
+#include "awq_kv_decode.cuh"
+#include "awq_kv_prefill.cuh"
 
 namespace {
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+awq_status cuda_status(cudaError_t e) { return e == cudaSuccess ? AWQ_OK : AWQ_ERR_CUDA; }
+
+// The current device's SM count, queried once; it must be an sm_100 part.
+struct DevInfo {
+    int sms = 0, cc_major = 0;
+};
+awq_status device_info(DevInfo &out) {
+    static std::mutex mu;
+    static DevInfo known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return AWQ_ERR_CUDA;
+    std::lock_guard<std::mutex> lk(mu);
+    DevInfo &d = known[dev];
+    if (d.sms == 0 && (cudaDeviceGetAttribute(&d.cc_major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+                       cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)) {
+        d.sms = 0;
+        return AWQ_ERR_CUDA;
+    }
+    if (d.cc_major != 10) return AWQ_ERR_UNSUPPORTED;
+    out = d;
+    return AWQ_OK;
+}
+
+// cuTensorMapEncodeTiled through the runtime's driver entry point (no -lcuda).
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiledFn encode_fn() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
 
 bool kv_dtype_ok(int t) { return t >= AWQ_F32 && t <= AWQ_BF16; }
 
@@ -91,20 +151,22 @@ int rope_threads(int64_t items, bool interleaved) {
     return want < 32 ? 32 : (want > 128 ? 128 : (int)want);
 }
 
+// Blocks that stay, 1024 threads an SM.
 template <typename TI, typename TO>
-cudaError_t launch_rope(const awq::kv::RopeArgs &A, int64_t T, bool vec, int sms, cudaStream_t st) {
+cudaError_t launch_rope(const awq::kv::RopeArgs &A, bool vec, int sms, cudaStream_t st) {
     const int64_t items = (int64_t)A.x.heads * (vec ? awq::kv::rope_items(A.dim, A.r.rot, A.r.interleaved) : A.dim / 2);
     const int threads = rope_threads(items, A.r.interleaved);
-    const int64_t grid = std::min<int64_t>(T, (int64_t)sms * (1024 / threads));
-    auto kernel = A.r.interleaved ? (vec ? awq::kv::rope_kernel<TI, TO, true, true> : awq::kv::rope_kernel<TI, TO, true, false>)
-                                  : (vec ? awq::kv::rope_kernel<TI, TO, false, true> : awq::kv::rope_kernel<TI, TO, false, false>);
+    const int64_t grid = std::min<int64_t>(A.T, (int64_t)sms * (1024 / threads));
+    auto kernel = !vec              ? awq::kv::rope_any_kernel
+                  : A.r.interleaved ? awq::kv::rope_kernel<TI, TO, true>
+                                    : awq::kv::rope_kernel<TI, TO, false>;
     return launch_overlapped(kernel, dim3((unsigned)grid), threads, 0, st, A);
 }
 template <typename TI>
-cudaError_t launch_rope_to(const awq::kv::RopeArgs &A, int64_t T, bool vec, int sms, cudaStream_t st) {
-    if (A.y.dtype == awq::kv::kF32) return launch_rope<TI, float>(A, T, vec, sms, st);
-    if (A.y.dtype == awq::kv::kF16) return launch_rope<TI, __half>(A, T, vec, sms, st);
-    return launch_rope<TI, __nv_bfloat16>(A, T, vec, sms, st);
+cudaError_t launch_rope_to(const awq::kv::RopeArgs &A, bool vec, int sms, cudaStream_t st) {
+    if (A.y.dtype == awq::kv::kF32) return launch_rope<TI, float>(A, vec, sms, st);
+    if (A.y.dtype == awq::kv::kF16) return launch_rope<TI, __half>(A, vec, sms, st);
+    return launch_rope<TI, __nv_bfloat16>(A, vec, sms, st);
 }
 
 template <typename TI, typename TO, bool INTER>
@@ -120,7 +182,6 @@ cudaError_t launch_append_dim(const awq::kv::AppendArgs &A, dim3 grid, cudaStrea
 }
 template <typename TI>
 cudaError_t launch_append(const awq::kv::AppendArgs &A, dim3 grid, cudaStream_t st) {
-    if (A.q_out.dtype == awq::kv::kF32) return launch_append_dim<TI, float>(A, grid, st);
     if (A.q_out.dtype == awq::kv::kF16) return launch_append_dim<TI, __half>(A, grid, st);
     return launch_append_dim<TI, __nv_bfloat16>(A, grid, st);
 }
@@ -156,7 +217,7 @@ cudaError_t once_per_device(F set) {
 }
 
 // Most blocks of the decode attention's first kernel, and rows of a tile.
-constexpr int64_t kDecMaxGrid = 512, kDecMaxRows = 16;
+constexpr int64_t kDecMaxGrid = 512, kDecMaxRows = 32;
 struct DecWs {
     size_t ml_off, o_off, total;
 };
@@ -168,11 +229,11 @@ DecWs dec_ws(int D) {
     return w;
 }
 
-template <typename TQ, int D, int NT>
+template <typename TQ, int D, int NT, int GR>
 cudaError_t launch_decode_rows(awq::kv::dec::Args &A, int sms,
                                int64_t most_rows, cudaStream_t st) {
-    using S = awq::kv::dec::Shape<D, NT>;
-    auto kernel = awq::kv::dec::kv_decode_kernel<TQ, D, NT>;
+    using S = awq::kv::dec::Shape<D, NT, GR>;
+    auto kernel = awq::kv::dec::kv_decode_kernel<TQ, D, NT, GR>;
     A.rows = S::ROWS;
     A.tile = S::TILE;
     A.box_rows = std::min(A.C.page, S::TILE);
@@ -190,16 +251,21 @@ cudaError_t launch_decode_rows(awq::kv::dec::Args &A, int sms,
     A.by_segment = segments <= grid;
     e = launch_overlapped(kernel, dim3(grid), awq::kv::dec::THREADS, S::BYTES, st, mk, mv, (const awq::kv::dec::Args)A);
     if (e != cudaSuccess) return e;
-    return launch_overlapped(awq::kv::dec::kv_decode_join_kernel<TQ, D>,
-                             dim3(A.by_segment ? (unsigned)segments : grid, rows), 32 * awq::kv::dec::JOIN_WARPS, 0, st,
+    constexpr int W = awq::kv::dec::JOIN_WARPS;
+    if (A.by_segment)
+        return launch_overlapped(awq::kv::dec::kv_decode_join_kernel<TQ, D, W>, dim3((unsigned)segments, rows), 32 * W, 0, st,
+                                 (const awq::kv::dec::Args)A);
+    return launch_overlapped(awq::kv::dec::kv_decode_join_kernel<TQ, D, 1>, dim3(grid, (rows + W - 1) / W), 32 * W, 0, st,
                              (const awq::kv::dec::Args)A);
 }
-// Tiles of 8 query rows while a sequence has no more: half the products of 16.
+// Tiles of 8 query rows while a sequence has no more: half the products of 16.  Tiles of 32 take the keys once for two
+// groups of warps, which convert them each.
 template <typename TQ, int D>
 cudaError_t launch_decode(awq::kv::dec::Args &A, int sms,
                           int64_t most_rows, cudaStream_t st) {
-    if (most_rows <= 8) return launch_decode_rows<TQ, D, 1>(A, sms, most_rows, st);
-    return launch_decode_rows<TQ, D, 2>(A, sms, most_rows, st);
+    if (most_rows <= 8) return launch_decode_rows<TQ, D, 1, 1>(A, sms, most_rows, st);
+    if (most_rows <= 16) return launch_decode_rows<TQ, D, 2, 1>(A, sms, most_rows, st);
+    return launch_decode_rows<TQ, D, 2, 2>(A, sms, most_rows, st);
 }
 
 // The kernel for many rows: blocks of threads, and splits of the keys while they do not fill the machine.
@@ -249,7 +315,7 @@ cudaError_t launch_prefill(const awq::kv::dec::Args &P, int64_t most_rows, void 
                              (const awq::kv::pre::Args)A);
 }
 // Up to kDecRows rows of a sequence and key head the kernel for few rows, from there on the other.
-constexpr int64_t kDecRows = 16;
+constexpr int64_t kDecRows = 32;
 template <typename TQ, int D>
 cudaError_t launch_attention(awq::kv::dec::Args &A, int sms, int64_t most_rows, void *ws, cudaStream_t st) {
     if (most_rows <= kDecRows) return launch_decode<TQ, D>(A, sms, most_rows, st);
@@ -298,10 +364,9 @@ awq_status awq_rope_table(int64_t n_pos, int32_t rot_dim, double base, awq_rope_
     }
     DevInfo d;
     if (awq_status e = device_info(d)) return e;
-    int grid = blocks_for(n_pos * A.half, 256);
-    if (grid > 16 * d.sms) grid = 16 * d.sms;
+    const int grid = (int)std::min<int64_t>((n_pos * A.half + 255) / 256, 16 * d.sms);
     awq::kv::rope_table_kernel<<<grid, 256, 0, (cudaStream_t)stream>>>(A);
-    return last_launch();
+    return cuda_status(cudaGetLastError());
 }
 
 awq_status awq_rope(awq_rows x, awq_rows y, int64_t T, int32_t head_dim, const int32_t *positions, awq_rope_cfg r,
@@ -327,9 +392,9 @@ awq_status awq_rope(awq_rows x, awq_rows y, int64_t T, int32_t head_dim, const i
     const bool vec = kv_rows_aligned(x) && kv_rows_aligned(y) && head_dim % 8 == 0 &&
                      r.rot_dim % (A.r.interleaved ? 8 : 16) == 0;
     cudaStream_t st = (cudaStream_t)stream;
-    cudaError_t e = x.dtype == AWQ_F32   ? launch_rope_to<float>(A, T, vec, d.sms, st)
-                    : x.dtype == AWQ_F16 ? launch_rope_to<__half>(A, T, vec, d.sms, st)
-                                         : launch_rope_to<__nv_bfloat16>(A, T, vec, d.sms, st);
+    cudaError_t e = x.dtype == AWQ_F32   ? launch_rope_to<float>(A, vec, d.sms, st)
+                    : x.dtype == AWQ_F16 ? launch_rope_to<__half>(A, vec, d.sms, st)
+                                         : launch_rope_to<__nv_bfloat16>(A, vec, d.sms, st);
     return cuda_status(e);
 }
 
@@ -342,7 +407,7 @@ awq_status awq_kv_append(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows k, 
     if (r.table && !kv_rope_ok(r, c.head_dim)) return AWQ_ERR_INVALID_ARG;
     if (q.data) {
         if (!r.table || !kv_rows_in(q) || !kv_rows_out(q_out, T, c.head_dim) || !kv_rows_aligned(q) ||
-            !kv_rows_aligned(q_out) || q.dtype != k.dtype || q.heads != q_out.heads || q.heads > 65536)
+            !kv_rows_aligned(q_out) || q.dtype != k.dtype || q_out.dtype == AWQ_F32 || q.heads != q_out.heads || q.heads > 65536)
             return AWQ_ERR_INVALID_ARG;
         if (q.data == q_out.data && (q.dtype != q_out.dtype || q.token_stride != q_out.token_stride ||
                                      q.head_stride != q_out.head_stride))
@@ -357,7 +422,8 @@ awq_status awq_kv_append(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows k, 
     A.kv[0] = kv_rows(k);
     A.kv[1] = kv_rows(v);
     A.q = kv_rows(q);
-    A.q_out = kv_rows(q.data ? q_out : k);
+    A.q_out = kv_rows(q_out);
+    if (!q.data) A.q_out.dtype = awq::kv::kF16;
     A.r = r.table ? kv_rope(r) : awq::kv::Rope{nullptr, 0, 0, 0};
     const int chunk = b.cu_tokens ? 16 : 1, teams = awq::kv::kAppendThreads / 32 / (b.cu_tokens ? 4 : 1);
     const int64_t chunks = (T + chunk - 1) / chunk;
@@ -412,7 +478,7 @@ awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows 
     A.meta = static_cast<awq::kv::dec::Meta *>(ws);
     A.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.ml_off);
     A.part_o = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + w.o_off);
-    A.timeout_ns = (uint64_t)g_timeout_ms.load() * 1000000ull;
+    A.timeout_ns = (uint64_t)awq_host::wait_timeout_ms() * 1000000ull;
     const int64_t most = (int64_t)max_tokens * A.group;
     cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
@@ -423,7 +489,13 @@ awq_status awq_kv_attention(awq_kv_cache c, awq_kv_batch b, int64_t T, awq_rows 
         e = q.dtype == AWQ_F16 ? launch_attention<__half, 128>(A, d.sms, most, ws, st)
                                : launch_attention<__nv_bfloat16, 128>(A, d.sms, most, ws, st);
     if (e != cudaSuccess) return AWQ_ERR_CUDA;
-    return last_launch();
+    return cuda_status(cudaGetLastError());
 }
 
 }  // extern "C"
+
+bool awq_host::take_kv_errors(unsigned *flags) {
+    if (cudaMemcpyFromSymbol(flags, awq::g_dev_error, sizeof(*flags)) != cudaSuccess) return false;
+    const unsigned zero = 0;
+    return !*flags || cudaMemcpyToSymbol(awq::g_dev_error, &zero, sizeof(zero)) == cudaSuccess;
+}

@@ -2,11 +2,11 @@
 // tokens and short drafts (sm_100a).  See awq_kv.cuh for the cache.
 //
 // A step reads every key and value once and does 4 * rows operations per byte, so
-// HBM bounds it: rows <= 16 keep the tensor cores far from their rate, and what
+// HBM bounds it: rows <= 32 keep the tensor cores far from their rate, and what
 // matters is that the codes stream without a pause and that the instructions to
 // turn them into operands fit beside the stream (an SM takes in 27 bytes a clock).
 //
-//  * Work.  A unit is 64 keys (128 for D = 64) of one (sequence, key head, tile of 8 or 16 rows); a
+//  * Work.  A unit is 64 keys (128 for D = 64) of one (sequence, key head, tile of 8, 16 or 32 rows); a
 //    row is (new token, query head of the key head's group), so a group shares each
 //    key.  The units of a launch, in order, are cut into equal contiguous ranges,
 //    one per block of threads (two or three blocks an SM), whatever the lengths: a ragged
@@ -53,22 +53,24 @@ constexpr int WARPS = 4;                   // consumer warps
 constexpr int THREADS = 32 * (WARPS + 1);
 constexpr float kLift = 9.0f, kSlack = 6.0f;       // see Scales above
 
-// NT tiles of 8 query rows.
-template <int D, int NT> struct Shape {
-    static constexpr int ROWS = 8 * NT;
+// NT tiles of 8 query rows a warp, GR groups of warps with rows of their own.
+template <int D, int NT, int GR> struct Shape {
+    static constexpr int ROWS = 8 * NT * GR;
     static constexpr int BLOCKS = NT == 1 ? 3 : 2;         // resident per SM: 128 or 168 registers a thread
-    static constexpr int TILE = 8192 / D;                  // keys per unit and stage
+    static constexpr int TILE = GR == 2 ? 64 : 8192 / D;   // keys per unit and stage
     static constexpr int NB = TILE / kBlock;               // blocks of scales of a unit
-    static constexpr int TURNS = 2 * WARPS / NB;           // 32 keys a warp: every unit (D = 64), or every other
+    static constexpr int PARTS = NB / 2;                   // warps that share a unit's keys, 32 each
+    static constexpr int TURNS = WARPS / GR / PARTS;       // 2: a warp takes every other unit
+    static constexpr int SUMS = WARPS / GR;                // warps whose sums of a row are joined
     static constexpr int STAGE = 2 * TILE * D;             // keys, values
-    static constexpr int STAGES = 4;
-    static_assert(STAGES % TURNS == 0, "a stage's phases must all be waited for by the same warps");
+    static constexpr int STAGES = 4 * (16384 / STAGE);
+    static_assert(TURNS >= 1 && STAGES % TURNS == 0, "a stage's phases must all be waited for by the same warps");
     static constexpr int PER = D / 8;                      // elements of a row that one lane holds
     static constexpr int LD = D + 36;                      // row of the merge area: 4 floats after every PER, 4 more
     static constexpr int OFF_SCALES = STAGES * STAGE;      // float [STAGES][2 * NB]
     static constexpr int OFF_BARS = OFF_SCALES + STAGES * 2 * NB * 4;
-    static constexpr int OFF_ML = OFF_BARS + STAGES * 16;  // float [WARPS][ROWS][2]
-    static constexpr int OFF_O = OFF_ML + WARPS * ROWS * 8;
+    static constexpr int OFF_ML = OFF_BARS + STAGES * 16;  // float [SUMS][ROWS][2]
+    static constexpr int OFF_O = OFF_ML + SUMS * ROWS * 8;
     static constexpr int BYTES = OFF_O + ROWS * LD * 4 + 1024;     // + alignment
 };
 
@@ -85,7 +87,7 @@ struct Args {
     int64_t window;
     float *lse;
     int group;                             // query heads per key head
-    int rows, tile;                        // query rows per tile, keys per unit
+    int rows, tile;                        // query rows per tile (8, 16 or 32), keys per unit
     int box_rows;                          // keys per TMA box: min(page, tile)
     // Where the join finds a split segment: by its own number (b heads + head) rt_most + rt while those are
     // fewer than the blocks (by_segment), else by the block that starts it (at most one split segment each).
@@ -320,10 +322,10 @@ template <int D> __device__ __forceinline__ uint32_t chunk_at(uint32_t row, uint
     return D == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4);
 }
 
-template <typename TQ, int D, int NT>
-__global__ void __launch_bounds__(THREADS, Shape<D, NT>::BLOCKS)
+template <typename TQ, int D, int NT, int GR>
+__global__ void __launch_bounds__(THREADS, Shape<D, NT, GR>::BLOCKS)
 kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_constant__ CUtensorMap tmap_v, const Args A) {
-    using S = Shape<D, NT>;
+    using S = Shape<D, NT, GR>;
     constexpr int ROWS = S::ROWS;
     extern __shared__ uint8_t raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
@@ -338,7 +340,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         found[0] = found[1] = 0;
         for (int i = 0; i < S::STAGES; ++i) {
             mbar_init(full + i, 4 * S::NB);
-            mbar_init(empty + i, S::NB / 2);
+            mbar_init(empty + i, WARPS / S::TURNS);
         }
         fence_mbar_init();
     }
@@ -430,7 +432,8 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     }
 
     // ---- consumers: 32 keys of a unit each; TURNS = 2: warps 0, 1 every other unit, warps 2, 3 the ones between
-    const int g = lane >> 2, c = lane & 3, part = warp % (S::NB / 2);
+    const int g = lane >> 2, c = lane & 3, part = warp % S::PARTS, group = GR == 1 ? 0 : warp / S::SUMS;
+    const int own = 8 * NT * group, sums_at = warp % S::SUMS;      // this warp's first row of a tile; its place in the join
     constexpr int NJ = D / 16;                                     // 16-row tiles of the second product
     constexpr int KB = NT == 1 ? 2 : 1;                            // blocks of 16 keys taken at once (registers)
     uint32_t qf[NT][D / 16][2];
@@ -443,12 +446,13 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     bool ok = true;
     for (int64_t done = R.first; done < R.end;) {
         // ---- a segment, or this block's part of it
-        const int n = cur.p.s.n, row0 = cur.rt * ROWS;
+        const int n = cur.p.s.n, row0 = cur.rt * ROWS + own;
         int all_lo, all_hi;                                        // keys that every row of the tile sees
         {
-            int last = (row0 + ROWS - 1) / A.group;
+            int last = (row0 + 8 * NT - 1) / A.group, first = row0 / A.group;
             if (last >= n) last = n - 1;
-            const int64_t p0 = cur.p.s.start + row0 / A.group + 1, p1 = cur.p.s.start + last + 1 - A.window;
+            if (first >= n) first = n - 1;
+            const int64_t p0 = cur.p.s.start + first + 1, p1 = cur.p.s.start + last + 1 - A.window;
             all_hi = p0 < 0 ? 0 : (p0 < cur.p.hi ? (int)p0 : cur.p.hi);
             all_lo = A.window && p1 > 0 ? (p1 < kMaxLen ? (int)p1 : (int)kMaxLen) : 0;
         }
@@ -474,7 +478,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         int first_key = (cur.p.t0 + (int)(done - cur.seg0)) * S::TILE + 32 * part;
         int turn = (int)((done - R.first) & 1);
         for (int left = units; left > 0; --left, first_key += S::TILE, turn ^= 1) {
-            if (S::TURNS == 1 || turn == warp / 2) {
+            if (S::TURNS == 1 || turn == warp / S::PARTS) {
                 // a wait that ran out skips the keys but not the barriers below
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(full + stage, phase, &abort_flag, A.timeout_ns));
 #pragma unroll 1
@@ -645,7 +649,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             }
         }
         done += units;
-        // ---- join the four warps: each brings its sums to the common reference and adds them in turn
+        // ---- join the warps: each brings its sums to the common reference and adds them in turn
         float *ml = reinterpret_cast<float *>(sm + S::OFF_ML), *oa = reinterpret_cast<float *>(sm + S::OFF_O);
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -656,22 +660,25 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 sum += __shfl_xor_sync(0xffffffffu, sum, 8);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 16);
                 if (g == 0) {
-                    float *p = ml + (warp * ROWS + 8 * t + 2 * c + x) * 2;
+                    float *p = ml + (sums_at * ROWS + own + 8 * t + 2 * c + x) * 2;
                     p[0] = (has >> (2 * t + x)) & 1 ? base[t][x] : -INFINITY;
                     p[1] = sum;
                 }
             }
         consumers_sync();
         auto common = [&](int r) {
-            return fmaxf(fmaxf(ml[2 * r], ml[2 * (ROWS + r)]), fmaxf(ml[2 * (2 * ROWS + r)], ml[2 * (3 * ROWS + r)]));
+            float m = ml[2 * r];
+#pragma unroll
+            for (int w = 1; w < S::SUMS; ++w) m = fmaxf(m, ml[2 * (w * ROWS + r)]);
+            return m;
         };
-        for (int w = 0; w < WARPS; ++w) {
-            if (w == warp) {
+        for (int w = 0; w < S::SUMS; ++w) {
+            if (w == sums_at) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int x = 0; x < 2; ++x) {
-                        const int r = 8 * t + 2 * c + x;
+                        const int r = own + 8 * t + 2 * c + x;
                         const float f = (has >> (2 * t + x)) & 1 ? ex2(base[t][x] - common(r)) : 0.0f;
                         float *row = oa + r * S::LD + g * (S::PER + 4);
 #pragma unroll
@@ -697,7 +704,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             const float mx = common(r);
             float L = 0.0f;
 #pragma unroll
-            for (int w = 0; w < WARPS; ++w) {
+            for (int w = 0; w < S::SUMS; ++w) {
                 const float mw = ml[(w * ROWS + r) * 2];
                 if (mw > -INFINITY) L = __fmaf_rn(ex2(mw - mx), ml[(w * ROWS + r) * 2 + 1], L);
             }
@@ -733,21 +740,23 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     }
 }
 
-// One block of threads per (split segment, row): its parts, summed in order.  Eight
-// warps take every eighth part; all of a warp's loads are on their way together.
+// The parts of a split segment's row, summed in order.  WPR warps a row: eight where there are few segments, each of
+// many parts (by_segment), one where there are many, of two or three parts as a rule; a warp's loads are all on their
+// way together.
 constexpr int JOIN_WARPS = 8;
-template <typename TQ, int D>
+template <typename TQ, int D, int WPR>
 __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_decode_join_kernel(const Args A) {
     constexpr int N = D / 32, DEEP = 8;
-    __shared__ float sl[JOIN_WARPS], so[JOIN_WARPS][D];
+    __shared__ float sm[JOIN_WARPS], sl[JOIN_WARPS], so[WPR == 1 ? 1 : WPR][D];
     griddep_launch_dependents();
     griddep_wait();
-    const int r = blockIdx.y;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int r = WPR == 1 ? blockIdx.y * JOIN_WARPS + warp : blockIdx.y, part = WPR == 1 ? 0 : warp;
     Meta M;
     Seq s;
     if (A.by_segment) {
         const int rt = blockIdx.x % A.rt_most, bh = blockIdx.x / A.rt_most;
-        s = seq_info(A.B, bh / A.C.heads, A.T, A.max_tokens);                    // beside the load of M
+        s = seq_info(A.B, bh / A.C.heads, A.T, A.max_tokens);      // beside the load of M
         M = A.meta[blockIdx.x];
         if ((int64_t)rt * A.rows >= (int64_t)s.n * A.group) return;      // there is no such segment
         if (M.last < 0) return;
@@ -757,16 +766,15 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_decode_join_kernel(const A
         s = seq_info(A.B, M.b, A.T, A.max_tokens);
     }
     const int row = M.rt * A.rows + r, tok = row / A.group, hq = M.head * A.group + row % A.group;
-    if (tok >= s.n) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (r >= A.rows || tok >= s.n) return;
     auto slot_of = [&](int i) { return ((int64_t)i * 2 + (i == M.first ? 1 : 0)) * A.rows + r; };
     float mx = -INFINITY, L = 0.0f, v[N] = {};                     // mx: reference of L and v
-    for (int i0 = M.first + warp; i0 <= M.last; i0 += JOIN_WARPS * DEEP) {
+    for (int i0 = M.first + part; i0 <= M.last; i0 += WPR * DEEP) {
         float2 p[DEEP];
         float x[DEEP][N];
 #pragma unroll
         for (int k = 0; k < DEEP; ++k) {
-            const int i = i0 + k * JOIN_WARPS;
+            const int i = i0 + k * WPR;
             p[k] = make_float2(-INFINITY, 0.0f);
             if (i <= M.last) {
                 p[k] = *reinterpret_cast<const float2 *>(A.part_ml + slot_of(i) * 2);
@@ -791,29 +799,30 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_decode_join_kernel(const A
             }
         mx = top;
     }
-    __shared__ float sm[JOIN_WARPS];
-    if (lane == 0) {
-        sm[warp] = mx;
-        sl[warp] = L;
-    }
-#pragma unroll
-    for (int n = 0; n < N; ++n) so[warp][lane * N + n] = v[n];
-    __syncthreads();
-    if (warp) return;
-    mx = sm[0];
-#pragma unroll
-    for (int w = 1; w < JOIN_WARPS; ++w) mx = fmaxf(mx, sm[w]);
-    L = 0.0f;
-#pragma unroll
-    for (int n = 0; n < N; ++n) v[n] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < JOIN_WARPS; ++w)
-        if (sm[w] > -INFINITY) {
-            const float f = ex2(sm[w] - mx);
-            L = __fmaf_rn(f, sl[w], L);
-#pragma unroll
-            for (int n = 0; n < N; ++n) v[n] = __fmaf_rn(f, so[w][lane * N + n], v[n]);
+    if (WPR > 1) {
+        if (lane == 0) {
+            sm[warp] = mx;
+            sl[warp] = L;
         }
+#pragma unroll
+        for (int n = 0; n < N; ++n) so[part][lane * N + n] = v[n];
+        __syncthreads();
+        if (warp) return;
+        mx = sm[0];
+#pragma unroll
+        for (int w = 1; w < WPR; ++w) mx = fmaxf(mx, sm[w]);
+        L = 0.0f;
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w)
+            if (sm[w] > -INFINITY) {
+                const float f = ex2(sm[w] - mx);
+                L = __fmaf_rn(f, sl[w], L);
+#pragma unroll
+                for (int n = 0; n < N; ++n) v[n] = __fmaf_rn(f, so[w][lane * N + n], v[n]);
+            }
+    }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll
     for (int n = 0; n < N; ++n) v[n] *= inv;

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 
 import torch
@@ -98,12 +99,16 @@ def _raw_stream(stream, device: int) -> int:
 
 
 def _where(t, device: int, name: str):
+    if not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
     raise ValueError(f"{name} is on {t.device}, expected cuda:{device}")
 
 
 def _rows(t: torch.Tensor, name: str, device: int) -> Rows:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+    if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
+    if t.get_device() != device:
+        _where(t, device, name)
     code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"{name} must be float32, float16 or bfloat16, got {t.dtype}")
@@ -113,8 +118,6 @@ def _rows(t: torch.Tensor, name: str, device: int) -> Rows:
     tok, head, one = t.stride()
     if one != 1:
         raise ValueError(f"{name} must have contiguous elements")
-    if t.get_device() != device:
-        _where(t, device, name)
     return Rows(t.data_ptr(), tok if T > 1 else H * D, head if H > 1 else D, H, code)
 
 
@@ -279,10 +282,16 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Ten
     return q_out if q is not None else None
 
 
-def kv_attention_workspace_bytes(cache: dict, T: int, q_heads: int, max_tokens: int = 1) -> int:
-    n, H, P, D = cache["k_codes"].shape
-    return int(_lib().awq_kv_attention_workspace_bytes(KVCache(None, None, None, None, n, P, H, D), T, q_heads,
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(heads: int, head_dim: int, q_heads: int, max_tokens: int) -> int:
+    return int(_lib().awq_kv_attention_workspace_bytes(KVCache(None, None, None, None, 1, 16, heads, head_dim), 1, q_heads,
                                                        max_tokens))
+
+
+def kv_attention_workspace_bytes(cache: dict, T: int, q_heads: int, max_tokens: int = 1) -> int:
+    """Bytes of `workspace` that kv_attention needs for these sizes."""
+    _, H, _, D = cache["k_codes"].shape
+    return _workspace_bytes(H, D, q_heads, max_tokens)
 
 
 def kv_attention(cache: dict, q: torch.Tensor, seq_lens: torch.Tensor, pages: torch.Tensor,
@@ -306,8 +315,9 @@ def kv_attention(cache: dict, q: torch.Tensor, seq_lens: torch.Tensor, pages: to
             raise ValueError("out must have q's shape")
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
         if T:
-            need = L.awq_kv_attention_workspace_bytes(C, T, H, max_tokens)
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device) if workspace is None else workspace
+            ws = workspace
+            if ws is None:
+                ws = torch.empty(_workspace_bytes(C.heads, D, H, max_tokens), dtype=torch.uint8, device=q.device)
             _check(L.awq_kv_attention(C, B, T, qr, _rows(out, "out", device),
                                       1.0 / math.sqrt(D) if scale is None else scale, max_tokens, window,
                                       lse.data_ptr() if return_lse else None, ws.data_ptr(), ws.numel(),

@@ -486,7 +486,7 @@ typedef struct {
  * way, and (optionally) rotate the same tokens' queries.
  *   k, v     rows of c.heads heads, one type
  *   rope     as in awq_rope, of the cache's positions; table NULL: no rotation
- *   q        rows of k's type, data NULL: none; q_out its rotated rows, any type
+ *   q        rows of k's type, data NULL: none; q_out its rotated rows, fp16 or bf16
  * Per block of 16 positions and head that gets tokens:
  *   e     the least exponent in [-40, 40] with |y| <= 448 * 2^e for every finite new
  *         value y (k rotated in binary32, or v), and not less than the exponent of
