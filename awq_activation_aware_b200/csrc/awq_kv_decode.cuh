@@ -71,7 +71,10 @@ template <int D, int NT, int GR> struct Shape {
     static constexpr int OFF_BARS = OFF_SCALES + STAGES * 2 * NB * 4;
     static constexpr int OFF_ML = OFF_BARS + STAGES * 16;  // float [SUMS][ROWS][2]
     static constexpr int OFF_O = OFF_ML + SUMS * ROWS * 8;
-    static constexpr int BYTES = OFF_O + ROWS * LD * 4 + 1024;     // + alignment
+    static constexpr bool Q_APART = NT > 1;                // query fragments in shared memory, a copy a warp: registers
+    static constexpr int OFF_Q = (OFF_O + ROWS * LD * 4 + 15) / 16 * 16;   // uint2 [WARPS][NT][D / 16][32]
+    static constexpr int Q_BYTES = Q_APART ? NT * (D / 16) * 32 * 8 : 0;
+    static constexpr int BYTES = OFF_Q + WARPS * Q_BYTES + 1024;   // + alignment
 };
 
 struct Meta {                              // a segment whose units lie in the ranges of several blocks
@@ -435,8 +438,9 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     const int g = lane >> 2, c = lane & 3, part = warp % S::PARTS, group = GR == 1 ? 0 : warp / S::SUMS;
     const int own = 8 * NT * group, sums_at = warp % S::SUMS;      // this warp's first row of a tile; its place in the join
     constexpr int NJ = D / 16;                                     // 16-row tiles of the second product
-    constexpr int KB = NT == 1 ? 2 : 1;                            // blocks of 16 keys taken at once (registers)
-    uint32_t qf[NT][D / 16][2];
+    constexpr int KB = 2;                                          // blocks of 16 keys taken at once
+    uint32_t qf[S::Q_APART ? 1 : NT][D / 16][2];
+    const uint32_t q_at = smem_u32(sm + S::OFF_Q + warp * S::Q_BYTES) + 8 * lane;
     float rowf[NT][2], base[NT][2], l[NT][2], o[NT][NJ][4];        // base: m - kLift of rows 2 c, 2 c + 1 of a tile,
     uint32_t has = 0;                                              // once they saw a key (bit 2 t + x), else 0
     bool settled = false;                                          // every row of the warp has
@@ -458,7 +462,12 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const float unscale = load_query<TQ, D>(A, cur, row0 + 8 * t + g, qf[t]) * A.scale_log2;
+            const float unscale = load_query<TQ, D>(A, cur, row0 + 8 * t + g, qf[S::Q_APART ? 0 : t]) * A.scale_log2;
+            if (S::Q_APART) {                                      // read back by the lane that wrote it
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(q_at + (t * (D / 16) + k) * 256), "r"(qf[0][k][0]), "r"(qf[0][k][1]) : "memory");
+            }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 rowf[t][x] = __shfl_sync(0xffffffffu, unscale, 4 * (2 * c + x));           // from the lane that loaded the row
@@ -509,7 +518,14 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                             for (int j = 0; j < 4; ++j) {
                                 const uint32_t a[4] = {cvt_lo(w0[j]), cvt_lo(w1[j]), cvt_hi(w0[j]), cvt_hi(w1[j])};
 #pragma unroll
-                                for (int t = 0; t < NT; ++t) mma_16816(s[b][t], a, qf[t][4 * i + j][0], qf[t][4 * i + j][1]);
+                                for (int t = 0; t < NT; ++t) {
+                                    if (S::Q_APART) {
+                                        const uint2 q = lds64(q_at + (t * (D / 16) + 4 * i + j) * 256);
+                                        mma_16816(s[b][t], a, q.x, q.y);
+                                    } else {
+                                        mma_16816(s[b][t], a, qf[t][4 * i + j][0], qf[t][4 * i + j][1]);
+                                    }
+                                }
                             }
                         }
                     // z = x + e - base, hidden keys -inf; 2^e = the value scale, inv_v = 2^-e
