@@ -122,9 +122,12 @@ __device__ __forceinline__ Span span_of(const Args &A, int b) {
     p.rt = (int)(((int64_t)p.s.n * A.group + A.rows - 1) / A.rows);
     return p;
 }
+// What a segment's start and end (query fragments, joining the warps, its first keys' latency) cost beside its units,
+// about 4500 clocks to their 1100: counted in, or blocks of threads that get many short sequences finish last.
+constexpr int kStart = 4;
 __device__ __forceinline__ int64_t units_of(const Args &A, int b) {
     const Span p = span_of(A, b);
-    return (int64_t)A.C.heads * p.rt * p.nt;
+    return (int64_t)A.C.heads * p.rt * (p.nt + kStart);
 }
 
 // Where a block's range starts, found by all threads: sums of units over the
@@ -194,33 +197,37 @@ __device__ __forceinline__ Range find_range(const Args &A, int64_t *sums, int64_
     return r;
 }
 
-// The block's place in its range: a run of tiles of one segment.
+// The block's place in its range.
 struct Cursor {
     int b, head, rt;
     Span p;
-    int64_t seg0;                          // first unit of the segment
-    int64_t u;                             // next unit
-    __device__ __forceinline__ void start(const Args &A, const Range &r) {
+    int64_t seg0;                          // number of the segment's first unit (kStart after the end of the one before)
+    int64_t u;                             // the block's first unit of it
+    // false: the range lies within the start of a segment, whose units are another block's
+    __device__ __forceinline__ bool start(const Args &A, const Range &r) {
         b = r.b;
         p = span_of(A, b);
-        u = r.first;
-        const int64_t i = (u - r.base) / p.nt;
-        seg0 = r.base + i * p.nt;
+        const int64_t i = (r.first - r.base) / (p.nt + kStart);
+        seg0 = r.base + i * (p.nt + kStart) + kStart;
+        u = r.first > seg0 ? r.first : seg0;
         head = (int)(i / p.rt);
         rt = (int)(i % p.rt);
+        return u < r.end;
     }
     __device__ __forceinline__ int64_t seg_end() const { return seg0 + p.nt; }
-    // to the segment that starts at seg_end() (there is one: it is below the range's end)
-    __device__ __forceinline__ void next(const Args &A) {
-        seg0 += p.nt;
+    // on to the next segment, if it has a unit below `end`
+    __device__ __forceinline__ bool next(const Args &A, int64_t end) {
+        if (seg_end() + kStart >= end) return false;
+        seg0 += p.nt + kStart;
         u = seg0;
-        if (++rt < p.rt) return;
+        if (++rt < p.rt) return true;
         rt = 0;
-        if (++head < A.C.heads) return;
+        if (++head < A.C.heads) return true;
         head = 0;
         do {
             p = span_of(A, ++b);
         } while (p.rt == 0);
+        return true;
     }
 };
 
@@ -354,7 +361,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     const Range R = find_range(A, sums, found);
     if (R.first >= R.end) return;
     Cursor cur;
-    cur.start(A, R);
+    if (!cur.start(A, R)) return;
 
     if (warp == WARPS) {
         // ---- the stream: 2 NB lanes for boxes of keys or values, 2 NB lanes for the blocks' scales
@@ -371,23 +378,27 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         };
         auto batch_of = [&](int64_t u) { return ((cur.p.t0 + (int)(u - cur.seg0)) * S::TILE >> page_bits) >> 5; };
         if (lane == 0 && cur.p.s.len > cur.p.hi) atomicOr(&g_dev_error, kDevErrBadIndex);
-        int hold_b = cur.b, hold_k = batch_of(R.first);
+        int hold_b = cur.b, hold_k = batch_of(cur.u);
         int32_t hold = fetch(hold_b, hold_k), ahead = fetch(hold_b, hold_k + 1);
         int stage = 0;
         uint32_t phase = 1;                                        // the first round finds the stages empty
         int64_t issued = 0;
-        bool ok = true;
-        for (int64_t u = R.first; u < R.end; ++u) {
+        bool ok = true, more = true;
+        for (int64_t u = cur.u; more;) {
             const int pos = (cur.p.t0 + (int)(u - cur.seg0)) * S::TILE + j * rows, head = cur.head;
             int64_t page = __shfl_sync(0xffffffffu, hold, (pos >> page_bits) & 31);
             if (!active || pos >= cur.p.hi) page = -1;             // nothing there
             else if (page < 0 || page >= A.C.n_pages) page = -2;   // a bad page
-            if (u + 1 < R.end) {                                   // the next unit's page numbers are on their way meanwhile
-                if (u + 1 == cur.seg_end()) {
-                    cur.next(A);
-                    if (lane == 0 && cur.p.s.len > cur.p.hi) atomicOr(&g_dev_error, kDevErrBadIndex);
-                }
-                const int k = batch_of(u + 1);
+            ++u;
+            if (u >= cur.seg_end()) {
+                more = cur.next(A, R.end);
+                u = cur.u;
+                if (more && lane == 0 && cur.p.s.len > cur.p.hi) atomicOr(&g_dev_error, kDevErrBadIndex);
+            } else {
+                more = u < R.end;
+            }
+            if (more) {                                            // the next unit's page numbers are on their way meanwhile
+                const int k = batch_of(u);
                 if (cur.b != hold_b || k != hold_k) {
                     hold = cur.b == hold_b && k == hold_k + 1 ? ahead : fetch(cur.b, k);
                     ahead = fetch(cur.b, k + 1);
@@ -448,7 +459,8 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
     int stage = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int64_t done = R.first; done < R.end;) {
+    int count = 0;                                                 // units of the segments before
+    do {
         // ---- a segment, or this block's part of it
         const int n = cur.p.s.n, row0 = cur.rt * ROWS + own;
         int all_lo, all_hi;                                        // keys that every row of the tile sees
@@ -483,9 +495,9 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         }
         has = 0;
         settled = false;
-        const int units = (int)((cur.seg_end() < R.end ? cur.seg_end() : R.end) - done);
-        int first_key = (cur.p.t0 + (int)(done - cur.seg0)) * S::TILE + 32 * part;
-        int turn = (int)((done - R.first) & 1);
+        const int units = (int)((cur.seg_end() < R.end ? cur.seg_end() : R.end) - cur.u);
+        int first_key = (cur.p.t0 + (int)(cur.u - cur.seg0)) * S::TILE + 32 * part;
+        int turn = count & 1;
         for (int left = units; left > 0; --left, first_key += S::TILE, turn ^= 1) {
             if (S::TURNS == 1 || turn == warp / S::PARTS) {
                 // a wait that ran out skips the keys but not the barriers below
@@ -664,7 +676,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 phase ^= 1;
             }
         }
-        done += units;
+        count += units;
         // ---- join the warps: each brings its sums to the common reference and adds them in turn
         float *ml = reinterpret_cast<float *>(sm + S::OFF_ML), *oa = reinterpret_cast<float *>(sm + S::OFF_O);
 #pragma unroll
@@ -752,8 +764,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                 {cur.b, cur.head, cur.rt, (int32_t)blockIdx.x, (int32_t)last};
         }
         consumers_sync();
-        if (done < R.end) cur.next(A);
-    }
+    } while (cur.next(A, R.end));
 }
 
 // The parts of a split segment's row, summed in order.  WPR warps a row: eight where there are few segments, each of

@@ -227,7 +227,7 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: 
     cfg = _rope_cfg(table, layout, device)
     with _on(device, stream):
         if out is None:
-            out = torch.empty((T, H, D), dtype=x.dtype if dtype is None else dtype, device=x.device)
+            out = x.new_empty((T, H, D), dtype=dtype)
         elif out.shape != x.shape or (dtype is not None and out.dtype != dtype):
             raise ValueError("out must have x's shape and the asked type")
         if T == 0:
@@ -273,7 +273,7 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Ten
             if q.shape[0] != T or q.shape[2] != D:
                 raise ValueError("q must have k's tokens and head_dim")
             if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q_dtype, device=k.device)
+                q_out = q.new_empty(q.shape, dtype=q_dtype)
             elif q_out.shape != q.shape:
                 raise ValueError("q_out must have q's shape")
             qo = _rows(q_out, "q_out", device)
@@ -310,14 +310,14 @@ def kv_attention(cache: dict, q: torch.Tensor, seq_lens: torch.Tensor, pages: to
     L = _lib()
     with _on(device, stream):
         if out is None:
-            out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+            out = q.new_empty((T, H, D))
         elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device) if return_lse else None
+        lse = q.new_empty((T, H), dtype=torch.float32) if return_lse else None
         if T:
             ws = workspace
             if ws is None:
-                ws = torch.empty(_workspace_bytes(C.heads, D, H, max_tokens), dtype=torch.uint8, device=q.device)
+                ws = q.new_empty(_workspace_bytes(C.heads, D, H, max_tokens), dtype=torch.uint8)
             _check(L.awq_kv_attention(C, B, T, qr, _rows(out, "out", device),
                                       1.0 / math.sqrt(D) if scale is None else scale, max_tokens, window,
                                       lse.data_ptr() if return_lse else None, ws.data_ptr(), ws.numel(),
