@@ -623,3 +623,141 @@ def test_attention_step_of_a_quantized_block(awq, new):
                             o["s_best"].cpu().numpy(), a_got.view(T, -1).cpu().numpy(), 4, 128)
         assert np.abs(f64(y) - Yr).max() <= 1e-4 * np.abs(Yr).max()
     awq.get_status()
+
+
+# ----- where the kernels change over, and what a hostile call could reach ---------
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,G", [(1, 8), (3, 3), (2, 8), (17, 1), (3, 8), (8, 4), (11, 3), (5, 8), (64, 2), (43, 3), (129, 2)])
+def test_attention_at_every_number_of_rows(awq, D, n, G):
+    """Rows a key head from 8 to 258: tiles of 8, 16 and 32 rows, then 128 and 256."""
+    c, q, lens, cu, pages = _attend_case(n * G + D, [n + 100, n + 700, n], [n, max(n - 1, 1), n], 2, G, D, 64)
+    _close(*_attend(awq, c, q, lens, cu, pages, BF16 if G % 2 else F16, D), BF16 if G % 2 else F16, D)
+
+
+@pytest.mark.parametrize("n", [1, 6, 40])
+def test_attention_of_many_short_sequences(awq, n):
+    """More sequences than blocks of threads, empty ones among them."""
+    rng = np.random.default_rng(n)
+    lens = rng.integers(0, 40, 700)
+    lens[::7] = 0
+    new = None if n == 1 else np.minimum(lens, rng.integers(0, n + 1, 700))
+    if new is not None:
+        new[0], lens[0] = n, max(lens[0], n)
+    c, q, lens, cu, pages = _attend_case(n, lens, new, 1, 4, 64, 16)
+    _close(*_attend(awq, c, q, lens, cu, pages, F16, 64), F16, 64)
+
+
+@pytest.mark.parametrize("n,G", [(4, 2), (8, 4), (40, 4)])
+def test_attention_nan_only_where_it_is_seen(awq, n, G):
+    """A value or key that is NaN reaches the rows that see it and no other."""
+    c, q, lens, cu, pages = _attend_case(50 + n, [150, 90], [n, n], 2, G, 128, 32)
+    clean = _attend(awq, c, q, lens, cu, pages, F16, 128)
+    hidden = 150 - n + n // 2                                              # seen by the later half of the first sequence's rows
+    for w, at in (("v", (pages[0, hidden // 32], 1, hidden % 32, 5)), ("k", (pages[0, hidden // 32], 0, hidden % 32, 9))):
+        d = {k: v.copy() for k, v in c.items()}
+        d[w + "_codes"][at] = 127
+        out, lse = _attend(awq, d, q, lens, cu, pages, F16, 128)[:2]
+        head = slice(G, 2 * G) if w == "v" else slice(0, G)
+        sees = torch.zeros(out.shape[:2], dtype=torch.bool, device="cuda")
+        sees[n // 2:n, head] = True
+        assert torch.equal(out[~sees], clean[0][~sees]) and torch.equal(lse[~sees], clean[1][~sees])
+        bad = torch.isnan(out[sees])
+        assert bool(bad[:, 5].all()) if w == "v" else bool(bad.all())
+
+
+@pytest.mark.parametrize("new", [[5, 3], [70, 3]])
+def test_attention_reports_more_tokens_than_promised(awq, new):
+    c, q, lens, cu, pages = _attend_case(60, [200, 90], new, 2, 4, 64, 32)
+    good = _attend(awq, c, q, lens, cu, pages, F16, 64)[0]
+    out = torch.full(q.shape, 7.0, device="cuda", dtype=F16)
+    awq.kv_attention(_upload(c), dev(q, F16), ints(lens), ints(pages), ints(cu), new[0] - 1, out=out)
+    with pytest.raises(awq.AWQError):
+        awq.get_status()
+    assert bool((out[:new[0]] == 7).all())                                 # not computed, not touched
+    d = f64(out[new[0]:]) - f64(good[new[0]:])
+    assert np.abs(d).max() <= 2.0 ** -9 * np.abs(f64(good)).max()          # the other sequence is (by another kernel, maybe)
+
+
+@pytest.mark.parametrize("new", [None, [6, 5], [90, 70]])
+def test_two_calls_at_once(awq, new):
+    """Two streams, each with its own workspace."""
+    cases = [_attend_case(70 + i, [1500, 700], new, 2, 4, 128, 64) for i in range(2)]
+    n = 1 if new is None else max(new)
+    alone = [_attend(awq, *c, F16, 128)[0] for c in cases]
+    args = [(_upload(c), dev(q, F16), ints(lens), ints(pages), None if cu is None else ints(cu), n)
+            for c, q, lens, cu, pages in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(8):
+        for i in range(2):
+            outs[i].append(awq.kv_attention(*args[i], stream=streams[i]))
+    torch.cuda.synchronize()
+    awq.get_status()
+    for i in range(2):
+        assert all(torch.equal(o, alone[i]) for o in outs[i])
+
+
+@pytest.mark.parametrize("new", [None, [3, 0, 40]])
+def test_a_captured_step_follows_its_inputs(awq, new):
+    """Append and attention captured together, replayed as the sequences grow, equal to the calls made one by one."""
+    rng = np.random.default_rng(80)
+    H, HQ, D, P = 2, 8, 64, 32
+    T = 3 if new is None else sum(new)
+    pages = rng.permutation(18).astype(np.int32).reshape(3, 6)
+    table = awq.rope_table(192, D)
+    cu = None if new is None else ints(np.concatenate([[0], np.cumsum(new)]))
+    n = 1 if new is None else max(new)
+    base = _random_cache(rng, 18, H, P, D)
+    live, ref = _upload(base), _upload(base)
+    x = torch.randn((T, HQ + 2 * H, D), device="cuda")
+    lens = ints([50, 1, 40])
+    out = torch.empty((T, HQ, D), device="cuda", dtype=F16)
+    ws = torch.empty(awq.kv_attention_workspace_bytes(live, T, HQ, n), dtype=torch.uint8, device="cuda")
+
+    def step(cache, out):
+        q = awq.kv_append(cache, x[:, HQ:HQ + H], x[:, HQ + H:], lens, ints_pages, cu, table, q=x[:, :HQ])
+        return awq.kv_attention(cache, q, lens, ints_pages, cu, n, out=out, workspace=ws)
+
+    ints_pages = ints(pages)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(_upload(base), out)                                           # kernels are loaded before the capture
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            step(live, out)
+    torch.cuda.synchronize()
+    for i in range(5):
+        x.copy_(torch.randn_like(x) * 2.0 ** i)
+        lens += 7 if new else 1
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        want = step(ref, torch.empty_like(out))
+        awq.get_status()
+        assert torch.equal(got, want)
+        for k in live:
+            a, b = (t[k].view(torch.uint8) if k.endswith("codes") else t[k] for t in (live, ref))
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 3, 9], [2, 4, 4, 40], [-3, 2, 5, 6]])
+def test_token_offsets_that_make_no_sense_stay_inside_the_arrays(awq, cu):
+    """Offsets that decrease, start late or pass the rows: whatever is computed, rows and pages outside are not touched."""
+    rng = np.random.default_rng(90)
+    c, _, _, _, pages = _attend_case(90, [40, 33, 60], None, 1, 2, 64, 16)
+    T = 8
+    x = torch.randn((T + 2, 4, 64), device="cuda", dtype=F16)
+    guard = torch.full((T + 2, 2, 64), 7.0, device="cuda", dtype=F16)
+    cache = _upload(c)
+    awq.kv_append(cache, x[:T, 2:3], x[:T, 3:], ints([40, 33, 60]), ints(pages), ints(cu), awq.rope_table(64, 64),
+                  q=x[:T, :2], q_out=guard[:T])
+    for most in (16, 40):
+        awq.kv_attention(cache, x[:T, :2], ints([40, 33, 60]), ints(pages), ints(cu), most, out=guard[:T])
+    torch.cuda.synchronize()
+    try:
+        awq.get_status()
+    except awq.AWQError:
+        pass
+    assert bool((guard[T:] == 7).all())
