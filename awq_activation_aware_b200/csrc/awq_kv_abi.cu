@@ -258,8 +258,8 @@ cudaError_t launch_decode_rows(awq::kv::dec::Args &A, int sms,
     return launch_overlapped(awq::kv::dec::kv_decode_join_kernel<TQ, D, 1>, dim3(grid, (rows + W - 1) / W), 32 * W, 0, st,
                              (const awq::kv::dec::Args)A);
 }
-// Tiles of 8 query rows while a sequence has no more: half the products of 16.  Tiles of 32 take the keys once for two
-// groups of warps, which convert them each.
+// Tiles of 8 query rows while a sequence has no more: half the products of 16 (131072 keys of 8 heads: 52 and 56 us).
+// Tiles of 32 take the keys once for two groups of warps, which convert them each (88 us).
 template <typename TQ, int D>
 cudaError_t launch_decode(awq::kv::dec::Args &A, int sms,
                           int64_t most_rows, cudaStream_t st) {
@@ -314,7 +314,9 @@ cudaError_t launch_prefill(const awq::kv::dec::Args &P, int64_t most_rows, void 
     return launch_overlapped(awq::kv::pre::kv_prefill_join_kernel<TQ, D>, dim3((unsigned)((warps + 7) / 8)), 256, 0, st,
                              (const awq::kv::pre::Args)A);
 }
-// Up to kDecRows rows of a sequence and key head the kernel for few rows, from there on the other.
+// Up to kDecRows rows of a sequence and key head the kernel for few rows, from there on the other: over 131072 keys of 8
+// heads the first takes 88 us with 32 rows, the other 122 with 40; over 8 sequences of 8000 keys 61 and 74.  More rows
+// would be a second tile, and every key read twice.
 constexpr int64_t kDecRows = 32;
 template <typename TQ, int D>
 cudaError_t launch_attention(awq::kv::dec::Args &A, int sms, int64_t most_rows, void *ws, cudaStream_t st) {

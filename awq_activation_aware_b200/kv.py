@@ -300,7 +300,8 @@ def kv_attention(cache: dict, q: torch.Tensor, seq_lens: torch.Tensor, pages: to
                  workspace: torch.Tensor | None = None, stream=None):
     """Causal attention of the new tokens' queries q [T, q_heads, head_dim] (fp16 or bf16) over the cache, their
     own keys appended before.  seq_lens, pages and cu_tokens as in kv_append; max_tokens bounds the new tokens of
-    any sequence.  scale defaults to head_dim^-0.5; window > 0 hides keys that far back.  Rows that see no key
+    any sequence (one with more is reported by get_status and not computed) and chooses the kernel for the whole batch:
+    single tokens beside long prompts are faster in a call of their own.  scale defaults to head_dim^-0.5; window > 0 hides keys that far back.  Rows that see no key
     give 0.  Returns out [T, q_heads, head_dim], with return_lse also the float32 log-sum-exp [T, q_heads]."""
     device = _cuda(q, "q")
     qr = _rows(q, "q", device)

@@ -506,10 +506,16 @@ AWQ_API awq_status awq_kv_append(awq_kv_cache cache, awq_kv_batch batch, int64_t
  * (lse -inf).  Scores, softmax statistics and sums are binary32; the products' operands
  * are exact (codes) or q's values; probabilities are rounded to fp16 for the second product.
  *   q, out      rows of q.heads heads (a multiple of c.heads), fp16 or bf16, the same type
- *   max_tokens  the most new tokens any sequence has (1 without cu_tokens)
+ *   max_tokens  the most new tokens any sequence has (1 without cu_tokens).  A sequence
+ *               with more raises AWQ_ERR_INVALID_ARG through awq_get_status(), and its
+ *               rows are not computed.  It also chooses the kernel, for the whole batch
+ *               (by max_tokens * q.heads / c.heads, up to 32 or more): single tokens
+ *               beside long prompts are faster in a call of their own
  *   lse         float [T, q.heads] or NULL: ln sum_j exp(scale q . k_j)
  *   ws          ws_bytes >= awq_kv_attention_workspace_bytes(...), 256-byte aligned;
  *               overwritten by every call: calls that share it must be ordered
+ * A NaN code reaches the rows that see its key, and no others.  Sequences have at most
+ * 2^30 tokens.  Make a first call of a kind before a stream capture: it loads the kernel.
  * Bases 16-byte aligned, strides multiples of 8 elements; out may not overlap q. */
 AWQ_API size_t awq_kv_attention_workspace_bytes(awq_kv_cache cache, int64_t T, int32_t q_heads,
                                                 int32_t max_tokens);
