@@ -138,6 +138,15 @@ def _ints(t: torch.Tensor, name: str, device: int, n: int) -> int:
     return t.data_ptr()
 
 
+def _buffer(t, name: str, device: int):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.uint8:
+        raise TypeError(f"{name} must be a uint8 CUDA tensor")
+    if t.get_device() != device:
+        _where(t, device, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
 def _cache(c: dict, device: int, D: int) -> KVCache:
     k, v, ks, vs = c["k_codes"], c["v_codes"], c["k_scales"], c["v_scales"]
     if k.dim() != 4 or v.shape != k.shape:
@@ -301,8 +310,10 @@ def kv_attention(cache: dict, q: torch.Tensor, seq_lens: torch.Tensor, pages: to
     """Causal attention of the new tokens' queries q [T, q_heads, head_dim] (fp16 or bf16) over the cache, their
     own keys appended before.  seq_lens, pages and cu_tokens as in kv_append; max_tokens bounds the new tokens of
     any sequence (one with more is reported by get_status and not computed) and chooses the kernel for the whole batch:
-    single tokens beside long prompts are faster in a call of their own.  scale defaults to head_dim^-0.5; window > 0 hides keys that far back.  Rows that see no key
-    give 0.  Returns out [T, q_heads, head_dim], with return_lse also the float32 log-sum-exp [T, q_heads]."""
+    single tokens beside long prompts are faster in a call of their own.  scale defaults to head_dim^-0.5; window > 0
+    hides keys that far back.  Rows that see no key give 0.  workspace: uint8, kv_attention_workspace_bytes, for
+    callers that keep one; calls that share it must be ordered.  Returns out [T, q_heads, head_dim], with return_lse
+    also the float32 log-sum-exp [T, q_heads]."""
     device = _cuda(q, "q")
     qr = _rows(q, "q", device)
     T, H, D = q.shape
@@ -319,6 +330,8 @@ def kv_attention(cache: dict, q: torch.Tensor, seq_lens: torch.Tensor, pages: to
             ws = workspace
             if ws is None:
                 ws = q.new_empty(_workspace_bytes(C.heads, D, H, max_tokens), dtype=torch.uint8)
+            else:
+                _buffer(ws, "workspace", device)
             _check(L.awq_kv_attention(C, B, T, qr, _rows(out, "out", device),
                                       1.0 / math.sqrt(D) if scale is None else scale, max_tokens, window,
                                       lse.data_ptr() if return_lse else None, ws.data_ptr(), ws.numel(),
@@ -334,7 +347,8 @@ def attention_step(x: torch.Tensor, qkv: dict, o: dict, cache: dict, seq_lens: t
     projection, the append with the rotation, the attention over the cache, and the packed output projection.
 
     qkv and o are packed layers (quantize_layer's or load_quantized's dicts); qkv stacks the rows of the q_heads
-    query heads, then of the cache's key heads, then of its value heads.  Returns float32 [T, rows of o]."""
+    query heads, then of the cache's key heads, then of its value heads.  Returns float32 [T, rows of o]; rows past the
+    last sequence (padding behind cu_tokens[n]) are not defined and touch no others."""
     from . import qlinear
     heads, D = cache["k_codes"].shape[1], cache["k_codes"].shape[3]
     if qkv["codes"].shape[0] != (q_heads + 2 * heads) * D:

@@ -576,6 +576,21 @@ def test_binding_refuses(awq):
     awq.get_status()
 
 
+def test_a_workspace_of_the_wrong_kind_is_refused(awq):
+    """Host memory, another type, every second byte: refused before anything is launched."""
+    cache, x = awq.kv_cache(4, 2, 16, 64), torch.zeros((2, 2, 64), device="cuda", dtype=F16)
+    lens, pages = ints([0, 0]), ints([[0], [1]])
+    n = awq.kv_attention_workspace_bytes(cache, 2, 2)
+    for ws, error in ((torch.empty(n, dtype=torch.uint8), TypeError),
+                      (torch.empty(n, dtype=torch.float32, device="cuda"), TypeError),
+                      (torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2], ValueError), (n, TypeError)):
+        with pytest.raises(error):
+            awq.kv_attention(cache, x, lens, pages, workspace=ws)
+    own = torch.empty(n, dtype=torch.uint8, device="cuda")
+    assert not bool(awq.kv_attention(cache, x, lens, pages, workspace=own).any())      # no keys: zeros
+    awq.get_status()
+
+
 # ----- a run of them together ----------------------------------------------------
 @pytest.mark.parametrize("new", [None, [40, 3]])
 def test_attention_step_of_a_quantized_block(awq, new):
