@@ -255,8 +255,8 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
     extern __shared__ uint8_t raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint64_t *bars = reinterpret_cast<uint64_t *>(sm + S::OFF_BAR);
-    uint64_t *qfull = bars, *sfull = bars + 2, *pfull = bars + 6, *pvdone = bars + 10, *drain = bars + 12,     // sfull, pfull: [tile][buffer]
-             *full = bars + 14, *empty = bars + 17, *rawfull = bars + 20, *rawempty = bars + 23;               // [RING]
+    uint64_t *qfull = bars, *sfull = bars + 2, *pfull = bars + 6, *pvdone = bars + 10, *drain = bars + 14,     // sfull, pfull, pvdone: [tile][buffer]
+             *full = bars + 16, *empty = bars + 19, *rawfull = bars + 22, *rawempty = bars + 25;               // [RING]
     __shared__ uint32_t tmem_base_sm;
     __shared__ int abort_sm;
     volatile int *abort_flag = &abort_sm;
@@ -266,7 +266,6 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         abort_sm = 0;
         for (int i = 0; i < 2; ++i) {
             mbar_init(qfull + i, 128);
-            mbar_init(pvdone + i, 1);
             mbar_init(drain + i, 1);
         }
         for (int i = 0; i < RING; ++i) {
@@ -278,6 +277,7 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
         for (int i = 0; i < 4; ++i) {
             mbar_init(sfull + i, 1);
             mbar_init(pfull + i, 128);
+            mbar_init(pvdone + i, 1);
         }
         fence_mbar_init();
     }
@@ -370,7 +370,7 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         l *= f;
                         if (j > 0 && __any_sync(0xffffffffu, f != 1.0f)) {
                             // the step before is the last whose product may still run: this one's P' is not out yet
-                            ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone + t, (j - 1) & 1, abort_flag, A.timeout_ns));
+                            ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone + 2 * t + (buf ^ 1), ((j - 1) >> 1) & 1, abort_flag, A.timeout_ns));
                             tc_fence_after();
 #pragma unroll
                             for (int ch = 0; ch < D / 32; ++ch) {
@@ -403,10 +403,9 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                     tc_fence_before();
                     mbar_arrive(pfull + 2 * t + buf);
                 }
-                // the last two products, in turn: a parity tells phase n only from n + 1, and of the earlier ones the last
-                // scores that arrived say that they are done
-                for (int j = w.ns > 1 ? w.ns - 2 : 0; j < w.ns && ok; ++j)
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(pvdone + t, j & 1, abort_flag, A.timeout_ns));
+                // All products: a barrier that fires once.  (Not the last phases of pvdone one after the other: a warp that
+                // comes late finds both complete, and a parity does not tell "two phases on" from "not yet".)
+                if (w.ns > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait_bounded(drain + t, 0, abort_flag, A.timeout_ns));
                 tc_fence_after();
                 if (ok) {
                     const float m = has ? base : -INFINITY;
@@ -557,7 +556,7 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
 #pragma unroll
                     for (int k = 1; k < STEP / 16; ++k)
                         mma_ts<kDescV>(o_tmem, s_tmem + 64 * buf + 8 * k, b + ((k * 2048) >> 4), PV, true);
-                    mma_commit_1(pvdone + t);
+                    mma_commit_1(pvdone + 2 * t + buf);
                     if (buf || j + 1 == w.ns) release(empty + st);
                 }
                 __syncwarp();

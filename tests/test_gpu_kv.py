@@ -591,6 +591,27 @@ def test_a_workspace_of_the_wrong_kind_is_refused(awq):
     awq.get_status()
 
 
+@pytest.mark.parametrize("D,G,new,past", [(128, 8, 40, 300), (64, 2, 150, 0), (128, 4, 9, 1500)])
+def test_many_calls_in_a_row_never_wait_in_vain(awq, D, G, new, past):
+    """Some millions of blocks of threads, launched as densely as a graph can: a wait that a late warp may miss runs
+    into its limit here (reported, and seen in the time), and all results are those of the first call."""
+    n, H = 48, 2
+    c, q, lens, cu, pages = _attend_case(71, [past + new + i % 5 for i in range(n)], [new] * n, H, G, D, 64)
+    cache, qd, l, u, p = _upload(c), dev(q, F16), ints(lens), ints(cu), ints(pages)
+    ws = torch.empty(awq.kv_attention_workspace_bytes(cache, q.shape[0], H * G, new), dtype=torch.uint8, device="cuda")
+    first = awq.kv_attention(cache, qd, l, p, u, new, workspace=ws)
+    out = torch.empty_like(first)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(100):
+            awq.kv_attention(cache, qd, l, p, u, new, workspace=ws, out=out)
+    for _ in range(100):
+        g.replay()
+    torch.cuda.synchronize()
+    awq.get_status()
+    assert torch.equal(out, first)
+
+
 # ----- a run of them together ----------------------------------------------------
 @pytest.mark.parametrize("new", [None, [40, 3]])
 def test_attention_step_of_a_quantized_block(awq, new):
