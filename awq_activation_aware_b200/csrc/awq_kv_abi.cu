@@ -252,13 +252,13 @@ cudaError_t launch_decode_rows(awq::kv::dec::Args &A, int sms,
     e = launch_overlapped(kernel, dim3(grid), awq::kv::dec::THREADS, S::BYTES, st, mk, mv, (const awq::kv::dec::Args)A);
     if (e != cudaSuccess) return e;
     constexpr int W = awq::kv::dec::JOIN_WARPS;
-    // launched plainly: blocks that wait for the first kernel's end take the registers that the next call's first kernel
-    // needs, which for many short segments costs more (24 sequences, 32 heads of 64, 2048 keys: 56 us a call, 41 without)
-    // than the early start brings (less than 1 us elsewhere)
-    if (A.by_segment)
-        awq::kv::dec::kv_decode_join_kernel<TQ, D, W><<<dim3((unsigned)segments, rows), 32 * W, 0, st>>>(A);
-    else
-        awq::kv::dec::kv_decode_join_kernel<TQ, D, 1><<<dim3(grid, (rows + W - 1) / W), 32 * W, 0, st>>>(A);
+    // Dim 64: the join is launched plainly.  Launched early it slows the calls around it down (32 heads of 64, window 2048,
+    // replayed back to back: 24 sequences 56 us a call, 41 plainly; 12: 33 and 27; 6: 24 and 18; why, the counters of a kernel
+    // by itself do not show).  Dim 128: an early start saves 1 to 2 us (131072 keys, calls in a row: 53.3 us, 55.0 plainly).
+    const dim3 joins = A.by_segment ? dim3((unsigned)segments, rows) : dim3(grid, (rows + W - 1) / W);
+    auto join = A.by_segment ? awq::kv::dec::kv_decode_join_kernel<TQ, D, W> : awq::kv::dec::kv_decode_join_kernel<TQ, D, 1>;
+    if (D == 128) return launch_overlapped(join, joins, 32 * W, 0, st, (const awq::kv::dec::Args)A);
+    join<<<joins, 32 * W, 0, st>>>(A);
     return cudaGetLastError();
 }
 // Tiles of 8 query rows while a sequence has no more: half the products of 16 (131072 keys of 8 heads: 52 and 56 us).

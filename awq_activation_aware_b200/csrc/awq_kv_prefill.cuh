@@ -28,8 +28,8 @@
 // With too few blocks of rows to fill the machine the keys are split over several
 // blocks of threads, and a second kernel joins their parts in order.
 //
-// Measured (device): 8192 new tokens, 32 query heads over 8, dim 128: 634 us, 867
-// TFLOP/s (dim 64: 517 us, 531); 512 tokens after 16000, 64 heads: 293 us, 930 TFLOP/s.
+// Measured (device): 8192 new tokens, 32 query heads over 8, dim 128: 625 us, 879
+// TFLOP/s (dim 64: 516 us, 533); 512 tokens after 16000, 64 heads: 290 us, 941 TFLOP/s.
 // What bounds it is the softmax beside the products: two warps a scheduler take 2350
 // clocks for 128 scores of a row by themselves and 2720 with the products running,
 // whose operands come through the same shared memory.
