@@ -121,6 +121,16 @@ def _rows(t: torch.Tensor, name: str, device: int) -> Rows:
     return Rows(t.data_ptr(), tok if T > 1 else H * D, head if H > 1 else D, H, code)
 
 
+def _new_rows(like: torch.Tensor, dtype: torch.dtype):
+    """Contiguous rows of like's shape, and their description (nothing of them needs a check but the type)."""
+    t = torch.empty_like(like, dtype=dtype, memory_format=torch.contiguous_format)
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"the result must be float32, float16 or bfloat16, got {dtype}")
+    _, H, D = t.shape
+    return t, Rows(t.data_ptr(), H * D, D, H, code)
+
+
 def _cuda(t, name: str) -> int:
     """The device of a CUDA tensor."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
@@ -160,11 +170,12 @@ def _cache(c: dict, device: int, D: int) -> KVCache:
         raise TypeError(f"k_scales and v_scales must be float32, got {ks.dtype} and {vs.dtype}")
     if ks.shape != (n, H, P // 16) or vs.shape != ks.shape:
         raise ValueError(f"k_scales and v_scales must be {(n, H, P // 16)}, got {tuple(ks.shape)} and {tuple(vs.shape)}")
-    for t in (k, v, ks, vs):
-        if t.get_device() != device:
-            _where(t, device, "the cache")
-        if not t.is_contiguous():
-            raise ValueError("the cache's tensors must be contiguous")
+    if not k.get_device() == v.get_device() == ks.get_device() == vs.get_device() == device:
+        for t in (k, v, ks, vs):
+            if t.get_device() != device:
+                _where(t, device, "the cache")
+    if not (k.is_contiguous() and v.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()):
+        raise ValueError("the cache's tensors must be contiguous")
     return KVCache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), n, P, H, D)
 
 
@@ -236,12 +247,14 @@ def rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, layout: 
     cfg = _rope_cfg(table, layout, device)
     with _on(device, stream):
         if out is None:
-            out = x.new_empty((T, H, D), dtype=dtype)
+            out, yr = _new_rows(x, dtype or x.dtype)
         elif out.shape != x.shape or (dtype is not None and out.dtype != dtype):
             raise ValueError("out must have x's shape and the asked type")
+        else:
+            yr = _rows(out, "out", device)
         if T == 0:
             return out
-        _check(_lib().awq_rope(xr, _rows(out, "out", device), T, D, pos, cfg, 1 if inverse else 0,
+        _check(_lib().awq_rope(xr, yr, T, D, pos, cfg, 1 if inverse else 0,
                                _raw_stream(stream, device)), "awq_rope")
     return out
 
@@ -282,10 +295,11 @@ def kv_append(cache: dict, k: torch.Tensor, v: torch.Tensor, seq_lens: torch.Ten
             if q.shape[0] != T or q.shape[2] != D:
                 raise ValueError("q must have k's tokens and head_dim")
             if q_out is None:
-                q_out = q.new_empty(q.shape, dtype=q_dtype)
+                q_out, qo = _new_rows(q, q_dtype)
             elif q_out.shape != q.shape:
                 raise ValueError("q_out must have q's shape")
-            qo = _rows(q_out, "q_out", device)
+            else:
+                qo = _rows(q_out, "q_out", device)
         if T:
             _check(_lib().awq_kv_append(C, B, T, kr, vr, qr, qo, cfg, _raw_stream(stream, device)), "awq_kv_append")
     return q_out if q is not None else None
@@ -322,9 +336,11 @@ def kv_attention(cache: dict, q: torch.Tensor, seq_lens: torch.Tensor, pages: to
     L = _lib()
     with _on(device, stream):
         if out is None:
-            out = q.new_empty((T, H, D))
+            out, outr = _new_rows(q, q.dtype)
         elif out.shape != q.shape:
             raise ValueError("out must have q's shape")
+        else:
+            outr = _rows(out, "out", device)
         lse = q.new_empty((T, H), dtype=torch.float32) if return_lse else None
         if T:
             ws = workspace
@@ -332,7 +348,7 @@ def kv_attention(cache: dict, q: torch.Tensor, seq_lens: torch.Tensor, pages: to
                 ws = q.new_empty(_workspace_bytes(C.heads, D, H, max_tokens), dtype=torch.uint8)
             else:
                 _buffer(ws, "workspace", device)
-            _check(L.awq_kv_attention(C, B, T, qr, _rows(out, "out", device),
+            _check(L.awq_kv_attention(C, B, T, qr, outr,
                                       1.0 / math.sqrt(D) if scale is None else scale, max_tokens, window,
                                       lse.data_ptr() if return_lse else None, ws.data_ptr(), ws.numel(),
                                       _raw_stream(stream, device)), "awq_kv_attention")

@@ -591,7 +591,8 @@ def test_a_workspace_of_the_wrong_kind_is_refused(awq):
     awq.get_status()
 
 
-@pytest.mark.parametrize("D,G,new,past", [(128, 8, 40, 300), (64, 2, 150, 0), (128, 4, 9, 1500)])
+@pytest.mark.parametrize("D,G,new,past", [(128, 8, 40, 300), (64, 2, 150, 0), (128, 4, 9, 1500), (128, 8, 1, 900),
+                                          (64, 1, 1, 700), (128, 4, 4, 200), (64, 8, 3, 1100)])
 def test_many_calls_in_a_row_never_wait_in_vain(awq, D, G, new, past):
     """Some millions of blocks of threads, launched as densely as a graph can: a wait that a late warp may miss runs
     into its limit here (reported, and seen in the time), and all results are those of the first call."""
