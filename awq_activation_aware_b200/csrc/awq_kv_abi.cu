@@ -130,6 +130,8 @@ awq::kv::Rope kv_rope(const awq_rope_cfg &r) {
 // A launch whose start may overlap the end of the kernel before it on the stream
 // (programmatic dependent launch): the kernel waits for that one (griddep_wait)
 // before it reads or writes anything in global memory, in every block of threads.
+// Calls in a row, with and without: rope of 16384 tokens 52.6 and 55.1 us, append of
+// seven prompts 87.0 and 89.9, of 256 single tokens (replayed) 6.5 and 7.2.
 template <typename... P>
 cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, P... args) {
     cudaLaunchConfig_t cfg = {};
