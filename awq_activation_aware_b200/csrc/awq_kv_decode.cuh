@@ -283,6 +283,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t w) {
 // Bytes of a word that hold a NaN code (0x7f or 0xff): 0x80 in each, else 0.
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
+// What a part of a row, of reference m, weighs beside the reference `top` of them all.  A part without a reference saw no
+// score but -inf or NaN: its sum is 0 or NaN.  Its sum is added like any other (0 * NaN is NaN), so a NaN stays.
+__device__ __forceinline__ float part_weight(float m, float top) { return m > -INFINITY ? ex2(m - top) : 0.0f; }
+
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory"); }
 
 // Query fragments (the 8-column operand) of row g of each tile: 16 neighbouring elements of
@@ -740,8 +744,7 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
             float L = 0.0f;
 #pragma unroll
             for (int w = 0; w < S::SUMS; ++w) {
-                const float mw = ml[(w * ROWS + r) * 2];
-                if (mw > -INFINITY) L = __fmaf_rn(ex2(mw - mx), ml[(w * ROWS + r) * 2 + 1], L);
+                L = __fmaf_rn(part_weight(ml[(w * ROWS + r) * 2], mx), ml[(w * ROWS + r) * 2 + 1], L);
             }
             const float4 *p = reinterpret_cast<const float4 *>(oa + r * S::LD + d + 4 * (d / S::PER));
             const float4 a = p[0], b = p[1];
@@ -818,19 +821,19 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_decode_join_kernel(const A
         float top = mx;
 #pragma unroll
         for (int k = 0; k < DEEP; ++k) top = fmaxf(top, p[k].x);
-        if (top == -INFINITY) continue;
-        const float f0 = ex2(mx - top);
+        const float f0 = part_weight(mx, top);
         L *= f0;
 #pragma unroll
         for (int n = 0; n < N; ++n) v[n] *= f0;
 #pragma unroll
-        for (int k = 0; k < DEEP; ++k)
+        for (int k = 0; k < DEEP; ++k) {
+            const float f = part_weight(p[k].x, top);
+            L = __fmaf_rn(f, p[k].y, L);
             if (p[k].x > -INFINITY) {
-                const float f = ex2(p[k].x - top);
-                L = __fmaf_rn(f, p[k].y, L);
 #pragma unroll
                 for (int n = 0; n < N; ++n) v[n] = __fmaf_rn(f, x[k][n], v[n]);
             }
+        }
         mx = top;
     }
     if (WPR > 1) {
@@ -849,13 +852,12 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv_decode_join_kernel(const A
 #pragma unroll
         for (int n = 0; n < N; ++n) v[n] = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WPR; ++w)
-            if (sm[w] > -INFINITY) {
-                const float f = ex2(sm[w] - mx);
-                L = __fmaf_rn(f, sl[w], L);
+        for (int w = 0; w < WPR; ++w) {
+            const float f = part_weight(sm[w], mx);
+            L = __fmaf_rn(f, sl[w], L);
 #pragma unroll
-                for (int n = 0; n < N; ++n) v[n] = __fmaf_rn(f, so[w][lane * N + n], v[n]);
-            }
+            for (int n = 0; n < N; ++n) v[n] = __fmaf_rn(f, so[w][lane * N + n], v[n]);
+        }
     }
     const float inv = L == 0.0f ? 0.0f : 1.0f / L;
 #pragma unroll

@@ -665,8 +665,7 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const Args A) {
         const float2 p = *reinterpret_cast<const float2 *>(A.part_ml + at * 2);
         float x[N];
         load_n(A.part_o + at * D + lane * N, x);
-        if (p.x == -INFINITY) continue;
-        const float f = ex2(p.x - mx);
+        const float f = dec::part_weight(p.x, mx);
         L = __fmaf_rn(f, p.y, L);
 #pragma unroll
         for (int n = 0; n < N; ++n) v[n] = __fmaf_rn(f, x[n], v[n]);

@@ -798,3 +798,49 @@ def test_token_offsets_that_make_no_sense_stay_inside_the_arrays(awq, cu):
     except awq.AWQError:
         pass
     assert bool((guard[T:] == 7).all())
+
+
+# ----- NaN queries and keys, wherever the work is cut -----------------------------
+def _close_but_nan(out, lse, ref, rl, info, dtype, D):
+    """As _close, but rows whose log-sum-exp is NaN have to be NaN in every element and in the log-sum-exp."""
+    bad = np.isnan(rl)
+    assert bad.any()
+    got, got_lse = f64(out), f64(lse)
+    assert np.isnan(got[bad]).all() and np.isnan(got_lse[bad]).all()
+    assert not np.isnan(got[~bad]).any() and not np.isnan(got_lse[~bad]).any()
+    fine = np.nonzero(~bad)
+    _close(out[fine], lse[fine], ref[fine], rl[fine], tuple(x[fine] for x in info), dtype, D)
+
+
+NAN_CASES = [  # lengths, new tokens, key heads, group, page columns beyond the sequences': what is cut how
+    ([40], None, 1, 4, 0), ([33], None, 2, 8, 0),                  # one unit of keys, two warps' parts of it
+    ([1000, 0, 300], None, 2, 4, 0), ([513], None, 8, 8, 0),       # segments cut, joined by segment
+    ([200] * 300, None, 2, 1, 0),                                  # more segments than blocks of threads
+    ([1000, 2, 300], [4, 5, 2], 2, 4, 0), ([900, 129], [8, 3], 2, 4, 0),     # drafts: tiles of 16 and 32 rows
+    ([90, 2], [90, 5], 2, 4, 0), ([700, 0, 300], [90, 0, 20], 2, 4, 0), ([513], [40], 1, 8, 40),   # the kernel for many rows
+]
+
+
+@pytest.mark.parametrize("D,dtype", [(128, F16), (64, BF16)])
+@pytest.mark.parametrize("lens,new,H,G,extra", NAN_CASES)
+def test_attention_of_nan_queries(awq, lens, new, H, G, extra, D, dtype):
+    """A NaN in a query, in one element or in all, is NaN in its row's result whatever the row is joined from; a row
+    without keys stays empty, and no other row is touched."""
+    c, q, lens, cu, pages = _attend_case(100 + len(lens) + G, lens, new, H, G, D, 32)
+    pages = np.concatenate([pages, np.full((len(lens), extra), 1 << 30, np.int32)], 1)
+    q[::2, 0], q[1::3, -1, 5], q[-1, (H * G) // 2, D - 1] = np.nan, np.nan, np.nan
+    _close_but_nan(*_attend(awq, c, q, lens, cu, pages, dtype, D), dtype, D)
+
+
+@pytest.mark.parametrize("D,dtype", [(128, F16), (64, BF16)])
+@pytest.mark.parametrize("lens,new,H,G,extra", NAN_CASES)
+@pytest.mark.parametrize("from_end", [1, 33])
+def test_attention_of_nan_keys(awq, lens, new, H, G, extra, D, dtype, from_end):
+    """A NaN in a sequence's last key (which opens a tile of its own where the length is 64 n + 1), or in one further
+    back: NaN in the rows that see it, and in their log-sum-exp."""
+    c, q, lens, cu, pages = _attend_case(200 + len(lens) + G, lens, new, H, G, D, 32)
+    pages = np.concatenate([pages, np.full((len(lens), extra), 1 << 30, np.int32)], 1)
+    for b, n in enumerate(lens):
+        if n >= from_end:
+            c["k_codes"][pages[b, (n - from_end) // 32], b % H, (n - from_end) % 32, 7] = 127
+    _close_but_nan(*_attend(awq, c, q, lens, cu, pages, dtype, D), dtype, D)
