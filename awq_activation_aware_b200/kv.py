@@ -15,6 +15,8 @@ import math
 
 import torch
 
+from .persist import _check_config
+
 __all__ = ["rope_table", "rope", "kv_cache", "kv_append", "kv_attention", "kv_attention_workspace_bytes",
            "attention_step"]
 
@@ -355,24 +357,56 @@ def kv_attention(cache: dict, q: torch.Tensor, seq_lens: torch.Tensor, pages: to
     return (out, lse) if return_lse else out
 
 
+def _packed(layer: dict, name: str, K: int, bits: int | None, group: int | None):
+    """Bits and group size of a packed layer of K inputs: its own, where it says them, else those given.  Its tensors
+    must have the shapes that these ask for: the kernel reads so many words a row."""
+    cfg = []
+    for key, given, usual in (("bits", bits, 4), ("group_size", group, 128)):
+        own = layer.get(key)
+        if own is not None and given is not None and own != given:
+            raise ValueError(f"{name} was packed with {key} {own}, asked for {given}")
+        cfg.append(own if own is not None else usual if given is None else given)
+    _check_config(*cfg, True)
+    b, g = cfg
+    N, per = layer["codes"].shape[0], 16 if b == 2 else 8
+    if K % g:
+        raise ValueError(f"{name}: {K} inputs are not groups of {g}")
+    for key, shape in (("codes", (N, K // per)), ("scales", (N, K // g)), ("zeros", (N, K // g)), ("s_best", (K,))):
+        if layer[key].shape != shape:
+            raise ValueError(f"{name}: {key} of {b} bits in groups of {g} over {K} inputs must be {shape}, "
+                             f"got {tuple(layer[key].shape)}")
+    return b, g
+
+
 def attention_step(x: torch.Tensor, qkv: dict, o: dict, cache: dict, seq_lens: torch.Tensor, pages: torch.Tensor,
                    table: torch.Tensor | None, q_heads: int, cu_tokens: torch.Tensor | None = None,
-                   max_tokens: int = 1, layout: str = "half", window: int = 0, bits: int = 4, group: int = 128,
-                   stream=None) -> torch.Tensor:
+                   max_tokens: int = 1, layout: str = "half", window: int = 0, bits: int | None = None,
+                   group: int | None = None, stream=None) -> torch.Tensor:
     """One attention block of a quantized model on its new tokens x [T, hidden] (fp16): the packed query/key/value
     projection, the append with the rotation, the attention over the cache, and the packed output projection.
 
     qkv and o are packed layers (quantize_layer's or load_quantized's dicts); qkv stacks the rows of the q_heads
-    query heads, then of the cache's key heads, then of its value heads.  Returns float32 [T, rows of o]; rows past the
+    query heads, then of the cache's key heads, then of its value heads.  A layer's own "bits" and "group_size"
+    (load_quantized's dicts have them) are what it is read with; `bits` and `group` stand for those of a layer
+    that does not say (4 and 128 if not given), and must agree with one that does.  Returns float32 [T, rows of o]; rows past the
     last sequence (padding behind cu_tokens[n]) are not defined and touch no others."""
     from . import qlinear
     heads, D = cache["k_codes"].shape[1], cache["k_codes"].shape[3]
     if qkv["codes"].shape[0] != (q_heads + 2 * heads) * D:
         raise ValueError(f"qkv has {qkv['codes'].shape[0]} rows, {q_heads} + 2 x {heads} heads of {D} need "
                          f"{(q_heads + 2 * heads) * D}")
-    T = x.shape[0]
-    with _on(_cuda(x, "x"), stream):
-        y = qlinear(qkv["codes"], qkv["scales"], qkv["zeros"], qkv["s_best"], x, bits, group, stream=stream)
+    if x.dim() != 2:
+        raise ValueError("x must be [tokens, hidden]")
+    T, hidden = x.shape
+    of_qkv = _packed(qkv, "qkv", hidden, bits, group)
+    of_o = _packed(o, "o", q_heads * D, bits, group)
+    device = _cuda(x, "x")
+    for layer, name in ((qkv, "qkv"), (o, "o")):
+        for key in ("codes", "scales", "zeros", "s_best"):
+            if layer[key].get_device() != device:
+                _where(layer[key], device, f"{name}'s {key}")
+    with _on(device, stream):
+        y = qlinear(qkv["codes"], qkv["scales"], qkv["zeros"], qkv["s_best"], x, *of_qkv, stream=stream)
         y = y.view(T, q_heads + 2 * heads, D)
         q, k, v = y[:, :q_heads], y[:, q_heads:q_heads + heads], y[:, q_heads + heads:]
         if table is None:
@@ -381,5 +415,5 @@ def attention_step(x: torch.Tensor, qkv: dict, o: dict, cache: dict, seq_lens: t
         else:
             qr = kv_append(cache, k, v, seq_lens, pages, cu_tokens, table, layout, q=q, stream=stream)
         a = kv_attention(cache, qr, seq_lens, pages, cu_tokens, max_tokens, window=window, stream=stream)
-        return qlinear(o["codes"], o["scales"], o["zeros"], o["s_best"], a.view(T, q_heads * D), bits, group,
+        return qlinear(o["codes"], o["scales"], o["zeros"], o["s_best"], a.view(T, q_heads * D), *of_o,
                        stream=stream)

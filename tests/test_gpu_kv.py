@@ -844,3 +844,41 @@ def test_attention_of_nan_keys(awq, lens, new, H, G, extra, D, dtype, from_end):
         if n >= from_end:
             c["k_codes"][pages[b, (n - from_end) // 32], b % H, (n - from_end) % 32, 7] = 127
     _close_but_nan(*_attend(awq, c, q, lens, cu, pages, dtype, D), dtype, D)
+
+
+# ----- steps of layers packed in other ways, and with the other options ------------
+@pytest.mark.parametrize("a,b,layout,window", [((2, 64), (4, 128), "interleaved", 0), ((4, 64), (2, 128), None, 5),
+                                               ((3, 128), (3, 64), "half", 20)])
+def test_attention_step_of_reloaded_layers(awq, tmp_path, a, b, layout, window):
+    """Layers packed with different bits and groups, saved and loaded: the step reads each as it was packed, and equals
+    its parts (layout None: no rotation)."""
+    from awq_activation_aware_b200 import persist, synth
+    HQ, H, D, hidden = 4, 2, 64, 384
+    layers = []
+    for i, (N, K, (bits, group)) in enumerate((((HQ + 2 * H) * D, hidden, a), (hidden, HQ * D, b))):
+        W, X, _ = synth.generate(synth.make_config(N, K, 256, bits=bits, group=group, seed=5 + i))
+        persist.save_quantized(tmp_path / "layer", awq.quantize_layer(dev(W), dev(X), bits=bits, group=group), bits, group)
+        layers.append(persist.load_quantized(tmp_path / "layer", "cuda"))
+    qkv, o = layers
+    lin = lambda q, x: awq.qlinear(q["codes"], q["scales"], q["zeros"], q["s_best"], x, q["bits"], q["group_size"])  # noqa: E731
+    table = awq.rope_table(64, D) if layout else None
+    pages = ints([[1, 0], [3, 2]])
+    cache, mine = (awq.kv_cache(4, H, 32, D) for _ in range(2))
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    for lens, cu, most in (([30, 7], [0, 30, 37], 30), ([31, 8], None, 1)):
+        T = 2 if cu is None else cu[-1]
+        x = torch.randn((T, hidden), device="cuda", generator=gen).half()
+        cu = None if cu is None else ints(cu)
+        y = awq.attention_step(x, qkv, o, cache, ints(lens), pages, table, HQ, cu, most, layout or "half", window)
+        z = lin(qkv, x).view(T, HQ + 2 * H, D)
+        q = awq.kv_append(mine, z[:, HQ:HQ + H], z[:, HQ + H:], ints(lens), pages, cu, table, layout or "half",
+                          q=z[:, :HQ] if layout else None)
+        at = awq.kv_attention(mine, q if layout else z[:, :HQ].half(), ints(lens), pages, cu, most, window=window)
+        assert torch.equal(y, lin(o, at.view(T, HQ * D)))
+        assert bool(torch.isfinite(y).all()) and bool(y.abs().max() > 0)
+    for bad in (dict(bits=a[0] - 1), dict(group=64 if a[1] == 128 else 128)):
+        with pytest.raises(ValueError):
+            awq.attention_step(x, qkv, o, cache, ints(lens), pages, table, HQ, **bad)
+    with pytest.raises(TypeError):                                         # a layer that is not on the device
+        awq.attention_step(x, qkv, o | dict(zeros=o["zeros"].cpu()), cache, ints(lens), pages, table, HQ)
+    awq.get_status()

@@ -204,3 +204,73 @@ def test_binding_refuses_host_tensors_and_unknown_names():
 def test_workspace_size_query_runs_without_a_gpu():
     n = awq.lib().awq_kv_attention_workspace_bytes(KVCache(**CACHE), 4, 32, 1)
     assert n > 0 and n % 256 == 0
+
+
+# ----- the configuration of the packed layers of a step ------------------------
+def _packed_layer(N, K, bits, group):
+    return dict(codes=torch.zeros((N, K // (16 if bits == 2 else 8)), dtype=torch.int32),
+                scales=torch.zeros((N, K // group), dtype=torch.float16),
+                zeros=torch.zeros((N, K // group), dtype=torch.float16), s_best=torch.ones(K))
+
+
+class _Reached(Exception):
+    pass
+
+
+def _step_reads(monkeypatch, qkv, o, K=256, **kw):
+    """(bits, group) that a step of 4 + 2 + 2 heads of 64 hands to each of its projections."""
+    calls = []
+
+    def qlinear(codes, scales, zeros, s_best, X, bits=4, group=128, **_):
+        calls.append((bits, group))
+        if len(calls) == 2:
+            raise _Reached
+        return torch.zeros((X.shape[0], codes.shape[0]))
+
+    monkeypatch.setattr(awq, "qlinear", qlinear)
+    monkeypatch.setattr(awq.kv, "_cuda", lambda t, name: -1)                # host tensors: device -1
+    monkeypatch.setattr(awq.kv, "_on", lambda *a: awq.kv._HERE)
+    monkeypatch.setattr(awq.kv, "kv_append", lambda *a, q=None, **k: q)
+    monkeypatch.setattr(awq.kv, "kv_attention", lambda cache, q, *a, **k: q.contiguous())
+    with pytest.raises(_Reached):
+        awq.attention_step(torch.zeros((3, K), dtype=torch.float16), qkv, o, awq.kv_cache(2, 2, 16, 64, device="cpu"),
+                           None, None, torch.zeros(1), 4, **kw)
+    return calls
+
+
+@pytest.mark.parametrize("a", [(2, 64), (3, 128), (4, 64), (4, 128)])
+@pytest.mark.parametrize("b", [(2, 128), (4, 128), (4, 64)])
+def test_a_step_reads_each_layer_as_it_was_packed(monkeypatch, a, b):
+    said = [dict(zip(("bits", "group_size"), x)) for x in (a, b)]
+    qkv, o = _packed_layer(512, 256, *a) | said[0], _packed_layer(320, 256, *b) | said[1]
+    assert _step_reads(monkeypatch, qkv, o) == [a, b]
+    # layers that do not say: what the call gives, 4 and 128 without
+    assert _step_reads(monkeypatch, _packed_layer(512, 256, *a), _packed_layer(320, 256, *a), bits=a[0], group=a[1]) == [a] * 2
+    plain = _packed_layer(512, 256, 4, 128), _packed_layer(320, 256, 4, 128)
+    assert _step_reads(monkeypatch, *plain) == [(4, 128)] * 2
+    assert _step_reads(monkeypatch, plain[0], o) == [(4, 128), b]
+
+
+def test_a_step_refuses_layers_that_it_would_misread():
+    """Refused by shapes and configuration alone, before anything is launched (these are host tensors)."""
+    x, cache = torch.zeros((3, 256), dtype=torch.float16), awq.kv_cache(2, 2, 16, 64, device="cpu")
+
+    def call(qkv={}, o={}, **kw):
+        qkv = _packed_layer(512, 256, 4, 128) | qkv
+        awq.attention_step(x, qkv, _packed_layer(320, 256, 4, 128) | o, cache, None, None, None, 4, **kw)
+
+    two = _packed_layer(512, 256, 2, 64)
+    bad = [dict(qkv=two), dict(o={k: v[:320] if v.dim() == 2 else v for k, v in two.items()}),      # 2 bits read as 4
+           dict(qkv=dict(bits=2)), dict(o=dict(bits=2)), dict(qkv=dict(group_size=64)), dict(o=dict(group_size=64)),
+           dict(qkv=dict(bits=4), bits=2), dict(o=dict(bits=4), bits=3), dict(o=dict(group_size=128), group=64),
+           dict(bits=2), dict(group=64), dict(bits=5), dict(group=32), dict(group=0), dict(qkv=dict(bits=8)),
+           dict(qkv=dict(s_best=torch.ones(128))), dict(o=dict(zeros=torch.zeros((320, 1), dtype=torch.float16))),
+           dict(o=dict(codes=torch.zeros((320, 16), dtype=torch.int32))),
+           dict(qkv=dict(scales=torch.zeros((511, 2), dtype=torch.float16)))]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            call(**kw)
+    with pytest.raises(ValueError):
+        awq.attention_step(x[0], _packed_layer(512, 256, 4, 128), _packed_layer(320, 256, 4, 128), cache, None, None, None, 4)
+    with pytest.raises(TypeError):                                         # the right shapes, on the host
+        call()
