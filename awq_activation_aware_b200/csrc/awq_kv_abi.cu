@@ -382,6 +382,7 @@ awq_status awq_rope(awq_rows x, awq_rows y, int64_t T, int32_t head_dim, const i
         (inverse != 0 && inverse != 1) || !kv_rope_ok(r, head_dim) || !kv_rows_in(x) || !kv_rows_out(y, T, head_dim) ||
         x.heads != y.heads)
         return AWQ_ERR_INVALID_ARG;
+    if ((int64_t)x.heads * head_dim > kMaxDim) return AWQ_ERR_INVALID_ARG;     // the kernels count a token's elements in 32 bits
     // in place: element for element the same memory, or another array altogether
     if (x.data == y.data &&
         (x.dtype != y.dtype || x.token_stride != y.token_stride || x.head_stride != y.head_stride))

@@ -24,6 +24,7 @@ _P, _i64, _i32, _f64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c
 _DTYPES = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
 _LAYOUTS = {"half": 0, "interleaved": 1}
 _SCALINGS = {None: 0, "none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+_MAX = (1 << 31) - 1                                       # of the ABI's 32-bit fields: ctypes would wrap what is larger
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
@@ -120,6 +121,8 @@ def _rows(t: torch.Tensor, name: str, device: int) -> Rows:
     tok, head, one = t.stride()
     if one != 1:
         raise ValueError(f"{name} must have contiguous elements")
+    if H * D > _MAX:
+        raise ValueError(f"{name}: {H} heads of {D} elements are counted in 32 bits")
     return Rows(t.data_ptr(), tok if T > 1 else H * D, head if H > 1 else D, H, code)
 
 
@@ -212,6 +215,8 @@ def _rope_cfg(table, layout, device: int) -> RopeCfg:
     if table.get_device() != device:
         _where(table, device, "table")
     n, half, _ = table.shape
+    if half > 32768:
+        raise ValueError(f"table: rot_dim must be at most 65536, got {2 * half}")
     return RopeCfg(table.data_ptr(), n, 2 * half, code)
 
 
@@ -225,6 +230,8 @@ def rope_table(n_pos: int, rot_dim: int, base: float = 10000.0, scaling: str | N
     0.1 ln(factor) + 1)."""
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling must be None, 'linear', 'ntk' or 'yarn', got {scaling!r}")
+    if rot_dim > 65536:
+        raise ValueError(f"rot_dim must be at most 65536, got {rot_dim}")
     device = torch.device(device)
     if device.type != "cuda":
         raise TypeError("the table lives on a CUDA device")
@@ -316,6 +323,8 @@ def _workspace_bytes(heads: int, head_dim: int, q_heads: int, max_tokens: int) -
 def kv_attention_workspace_bytes(cache: dict, T: int, q_heads: int, max_tokens: int = 1) -> int:
     """Bytes of `workspace` that kv_attention needs for these sizes."""
     _, H, _, D = cache["k_codes"].shape
+    if max_tokens > _MAX:
+        raise ValueError(f"max_tokens {max_tokens} does not fit 32 bits")
     return _workspace_bytes(H, D, q_heads, max_tokens)
 
 
@@ -335,6 +344,8 @@ def kv_attention(cache: dict, q: torch.Tensor, seq_lens: torch.Tensor, pages: to
     T, H, D = q.shape
     C = _cache(cache, device, D)
     B = _batch(seq_lens, pages, cu_tokens, T, device)
+    if max_tokens > _MAX:
+        raise ValueError(f"max_tokens {max_tokens} does not fit 32 bits")
     L = _lib()
     with _on(device, stream):
         if out is None:

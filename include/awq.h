@@ -437,8 +437,8 @@ AWQ_API awq_status awq_rope_table(int64_t n_pos, int32_t rot_dim, double base, a
  *              it was and raises AWQ_ERR_INVALID_ARG through awq_get_status().
  *   inverse    1: by minus the angle -- for a table of magnitude 1 the inverse, for
  *              every table the transpose, so also the gradient: dx = rope(dy, inverse)
- * x and y: any of the three types and any strides, head_dim even, rot_dim even and
- * <= head_dim; y may be x itself (same type and strides), otherwise they may not
+ * x and y: any of the three types and any strides, head_dim even, at most 65536 and
+ * heads * head_dim < 2^31, rot_dim even and <= head_dim; y may be x itself (same type and strides), otherwise they may not
  * overlap.  16-byte accesses where base and strides (multiples of 8 elements),
  * head_dim (8) and rot_dim (8; 16 in the half layout) allow them; y's base must be
  * aligned to its element in any case. */

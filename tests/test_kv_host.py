@@ -274,3 +274,31 @@ def test_a_step_refuses_layers_that_it_would_misread():
         awq.attention_step(x[0], _packed_layer(512, 256, 4, 128), _packed_layer(320, 256, 4, 128), cache, None, None, None, 4)
     with pytest.raises(TypeError):                                         # the right shapes, on the host
         call()
+
+
+# ----- sizes past 32 bits -------------------------------------------------------
+def test_rope_refuses_tokens_past_32_bits():
+    """Elements of a token are counted in 32 bits."""
+    L = awq.lib()
+
+    def call(heads, dim, rot=64):
+        x = dict(heads=heads, head_stride=dim, token_stride=heads * dim)
+        return L.awq_rope(Rows(**{**ROWS, **x}), Rows(**{**ROWS, **x, "data": 2 * P}), 16, dim, P,
+                          RopeCfg(**{**CFG, "rot_dim": rot}), 0, None)
+
+    for heads, dim in ((65536, 65536), (32768, 65536), (1 << 30, 2), ((1 << 31) - 1, 128)):
+        assert call(heads, dim, 2) == 1, (heads, dim)
+
+
+def test_binding_refuses_sizes_that_a_32_bit_field_would_wrap():
+    """On host tensors (device -1) of any size in no memory."""
+    one = torch.zeros((1, 1, 2), dtype=torch.float16)
+    assert awq.kv._rows(one, "x", -1).heads == 1
+    for shape in ((1, (1 << 32) + 1, 2), (1, 1 << 31, 2), (1, 1 << 30, 2), (5, 1 << 16, 1 << 15)):
+        x = torch.zeros(shape[2], dtype=torch.float16).expand(shape)
+        with pytest.raises(ValueError, match="32 bits"):
+            awq.kv._rows(x, "x", -1)
+    with pytest.raises(ValueError, match="rot_dim"):
+        awq.rope_table(1, (1 << 32) + 64)
+    with pytest.raises(ValueError, match="32 bits"):
+        awq.kv_attention_workspace_bytes(awq.kv_cache(1, 2, 16, 64, device="cpu"), 4, 2, (1 << 32) + 1)
