@@ -882,3 +882,59 @@ def test_attention_step_of_reloaded_layers(awq, tmp_path, a, b, layout, window):
     with pytest.raises(TypeError):                                         # a layer that is not on the device
         awq.attention_step(x, qkv, o | dict(zeros=o["zeros"].cpu()), cache, ints(lens), pages, table, HQ)
     awq.get_status()
+
+
+def _guarded(t, fill):
+    """t's values in the middle of a larger buffer, and that buffer's view as bytes."""
+    pad = 4096                                                             # bytes: keeps every alignment
+    raw = torch.full((t.numel() * t.element_size() + 2 * pad,), fill, dtype=torch.uint8, device="cuda")
+    mid = raw[pad:-pad].view(t.dtype).view(t.shape)
+    mid.copy_(t)
+    return mid, raw
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 3, 9], [2, 4, 4, 40], [-3, 2, 5, 6], [9, 9, 9, 9], [8, 6, 2, 0], [0, -5, 8, 8],
+                                [-(1 << 31), 3, 3, (1 << 31) - 1], [0, 3, 6, 8]])
+@pytest.mark.parametrize("lens", [[40, 33, 60], [-7, 0, 2], [(1 << 31) - 1, 47, -(1 << 31)]])
+def test_senseless_offsets_and_lengths_touch_nothing_else(awq, cu, lens):
+    """Append and attention (both kernels) with offsets that decrease, start late or pass the rows, and lengths past the
+    page table or below zero.  The memory around every array that is written, pages that no table names, and rows past
+    the given ones keep their bytes."""
+    rng = np.random.default_rng(91)
+    H, HQ, D, P, T = 1, 2, 64, 16, 8
+    base = _random_cache(rng, 16, H, P, D)
+    pages = np.array([[3, 14, 7, 9], [1, 12, 5, 11], [2, 6, 13, 8]], np.int32)      # 0, 4, 10 and 15 are nobody's
+    held = {k: _guarded(t.view(torch.uint8) if k.endswith("codes") else t, 0x5a) for k, t in _upload(base).items()}
+    cache = {k: v[0] for k, v in held.items()}
+    x = torch.randn((T + 2, HQ + 2 * H, D), device="cuda", dtype=F16)
+    table = awq.rope_table(64, D)
+    q_out, q_raw = _guarded(torch.zeros((T, HQ, D), dtype=F16), 0x5a)
+    out, out_raw = _guarded(torch.zeros((T, HQ, D), dtype=F16), 0x5a)
+    lse, lse_raw = _guarded(torch.zeros((T, HQ)), 0x5a)
+    awq.kv_append(cache, x[:T, HQ:HQ + H], x[:T, HQ + H:], ints(lens), ints(pages), ints(cu), table, q=x[:T, :HQ], q_out=q_out)
+    wide = torch.full((3, 9), 15, dtype=torch.int32, device="cuda")       # columns past max_pages name a page of nobody
+    wide[:, :4] = ints(pages)
+    raws = [raw for _, raw in held.values()] + [q_raw, out_raw, lse_raw]
+    for most in (1, 8, 16, 40):
+        n = awq.kv_attention_workspace_bytes(cache, T, HQ, most)
+        ws = torch.full((n + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+        seq, off = ints(lens), ints(cu)
+        code = awq.lib().awq_kv_attention(
+            awq.kv._cache(cache, 0, D), awq.kv._batch(seq, wide[:, :4], off, T, 0), T, awq.kv._rows(x[:T, :HQ], "q", 0),
+            awq.kv._rows(out, "out", 0), 0.125, most, 0, lse.data_ptr(), ws.data_ptr(), n,
+            torch.cuda.current_stream().cuda_stream)
+        assert code == 0
+        torch.cuda.synchronize()
+        assert bool((ws[n:] == 0x5a).all())
+    for raw in raws:
+        assert bool((raw[:4096] == 0x5a).all() and (raw[-4096:] == 0x5a).all())
+    for k, b in base.items():
+        got = cache[k].cpu().numpy()
+        np.testing.assert_array_equal(got[[0, 4, 10, 15]], b[[0, 4, 10, 15]], err_msg=k)
+        # no position of a page table is reached by a sequence without tokens in it
+        if lens == [-7, 0, 2]:
+            np.testing.assert_array_equal(got[[14, 7, 9, 12, 5, 11, 6, 13, 8]], b[[14, 7, 9, 12, 5, 11, 6, 13, 8]], err_msg=k)
+    try:
+        awq.get_status()
+    except awq.AWQError as e:
+        assert e.code == 1
