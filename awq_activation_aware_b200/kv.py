@@ -92,8 +92,13 @@ _HERE = contextlib.nullcontext()
 
 def _on(device: int, stream):
     """Context for a call on `device`: the tensors' device current, and memory
-    that the call allocates taken on the stream that uses it."""
-    return _HERE if stream is None and device == torch.cuda.current_device() else _enter(device, stream)
+    that the call allocates taken on the stream that uses it.  A stream of another
+    device is refused: its kernels would run there, on this device's memory."""
+    if stream is None:
+        return _HERE if device == torch.cuda.current_device() else _enter(device, None)
+    if stream.device.index != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on cuda:{device}")
+    return _enter(device, stream)
 
 
 def _raw_stream(stream, device: int) -> int:

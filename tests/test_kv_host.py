@@ -302,3 +302,19 @@ def test_binding_refuses_sizes_that_a_32_bit_field_would_wrap():
         awq.rope_table(1, (1 << 32) + 64)
     with pytest.raises(ValueError, match="32 bits"):
         awq.kv_attention_workspace_bytes(awq.kv_cache(1, 2, 16, 64, device="cpu"), 4, 2, (1 << 32) + 1)
+
+
+# ----- streams and devices -------------------------------------------------------
+class _Stream:
+    """What the binding asks of a stream, without a device."""
+    def __init__(self, index):
+        self.device, self.cuda_stream = torch.device("cuda", index), 0
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """A launch there would read and write this device's memory from the other one."""
+    monkeypatch.setattr(awq.kv, "_enter", lambda device, stream: ("entered", device))
+    assert awq.kv._on(0, _Stream(0)) == ("entered", 0) and awq.kv._on(3, _Stream(3)) == ("entered", 3)
+    for device, other in ((0, 1), (1, 0)):
+        with pytest.raises(ValueError, match="stream"):
+            awq.kv._on(device, _Stream(other))
