@@ -489,8 +489,12 @@ def awq_gptq(W: torch.Tensor, X: torch.Tensor, bits: int = 4, group: int = 128, 
 
 
 def get_status(stream=None) -> None:
-    """Synchronise and raise if a kernel reported an error on the device."""
-    _check(lib().awq_get_status(_stream(stream)), "awq_get_status")
+    """Synchronise and raise if a kernel reported an error on the device (the stream's; without one, the current)."""
+    if stream is None:
+        _check(lib().awq_get_status(_stream()), "awq_get_status")
+        return
+    with torch.cuda.device(stream.device):
+        _check(lib().awq_get_status(_stream(stream)), "awq_get_status")
 
 
 def selftest_bounded_wait(stream=None) -> None:

@@ -327,8 +327,8 @@ AWQ_API awq_status awq_pack(const void *W, int64_t N, int64_t K, const float *a,
 AWQ_API awq_status awq_pack_scales(const void *W, int64_t N, int64_t K, const float *s, awq_qcfg q,
                                    uint32_t *codes, void *scales, void *zeros, void *stream);
 
-/* Synchronises `stream`, then reports (and clears) errors raised on the device
- * since the last call: AWQ_ERR_TIMEOUT if a kernel's bounded wait ran out,
+/* Synchronises `stream`, then reports (and clears) errors raised on the current device
+ * (which has to be the stream's) since the last call: AWQ_ERR_TIMEOUT if a kernel's bounded wait ran out,
  * AWQ_ERR_INVALID_ARG if a kernel saw an alpha outside [0, 1], a given scale
  * that is not positive and finite, a Hessian that is not positive definite, or
  * a position or cache page outside its array, AWQ_ERR_CUDA for

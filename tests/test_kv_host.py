@@ -318,3 +318,28 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     for device, other in ((0, 1), (1, 0)):
         with pytest.raises(ValueError, match="stream"):
             awq.kv._on(device, _Stream(other))
+
+
+def test_status_is_read_on_the_streams_device(monkeypatch):
+    """Every device has its own error words: the ones of the stream's device are asked for."""
+    import contextlib
+    current, asked = [0], []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, current[0] = current[0], torch.device(d).index
+        yield
+        current[0] = before
+
+    class Lib:
+        @staticmethod
+        def awq_get_status(stream):
+            asked.append(current[0])
+            return 1 if current[0] == 1 else 0
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(awq, "lib", lambda: Lib)
+    awq.get_status(_Stream(0))
+    with pytest.raises(awq.AWQError):
+        awq.get_status(_Stream(1))
+    assert asked == [0, 1]
