@@ -507,22 +507,19 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
         has = 0;
         settled = false;
         const int units = (int)((cur.seg_end() < R.end ? cur.seg_end() : R.end) - cur.u);
-        int first_key = (cur.p.t0 + (int)(cur.u - cur.seg0)) * S::TILE + 32 * part;
+        int key0 = (cur.p.t0 + (int)(cur.u - cur.seg0)) * S::TILE + 32 * part;
         int turn = count & 1;
-        for (int left = units; left > 0; --left, first_key += S::TILE, turn ^= 1) {
+        for (int left = units; left > 0; --left, key0 += S::TILE, turn ^= 1) {
             if (S::TURNS == 1 || turn == warp / S::PARTS) {
                 // a wait that ran out skips the keys but not the barriers below
                 ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(full + stage, phase, &abort_flag, A.timeout_ns));
-#pragma unroll 1
-              for (int b0 = 0; b0 < 2; b0 += KB) {
-                const int key0 = first_key + 16 * b0;
                 float ks[KB], vs[KB];
 #pragma unroll
                 for (int b = 0; b < KB; ++b) {
-                    ks[b] = scales[stage * 2 * S::NB + 2 * part + b0 + b];
-                    vs[b] = scales[stage * 2 * S::NB + S::NB + 2 * part + b0 + b];
+                    ks[b] = scales[stage * 2 * S::NB + 2 * part + b];
+                    vs[b] = scales[stage * 2 * S::NB + S::NB + 2 * part + b];
                 }
-                const uint32_t kt = smem_u32(sm + stage * S::STAGE) + (32 * part + 16 * b0) * D, vt = kt + S::TILE * D;
+                const uint32_t kt = smem_u32(sm + stage * S::STAGE) + 32 * part * D, vt = kt + S::TILE * D;
                 const bool whole = key0 >= all_lo && key0 + 16 * KB <= all_hi && fminf(ks[0], ks[KB - 1]) >= 0.0f;
                 if (ok && (whole || key0 < cur.p.hi)) {
                     float s[KB][NT][4];                            // keys g (0, 1), g + 8 (2, 3) of rows 2 c, 2 c + 1
@@ -678,7 +675,6 @@ kv_decode_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_consta
                         }
                     }
                 }
-              }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty + stage);
             }
