@@ -287,12 +287,19 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7
 // score but -inf or NaN: its sum is 0 or NaN.  Its sum is added like any other (0 * NaN is NaN), so a NaN stays.
 __device__ __forceinline__ float part_weight(float m, float top) { return m > -INFINITY ? ex2(m - top) : 0.0f; }
 
+// 0, or NaN where a query's elements (fp16 pairs) are not all finite: 0 * inf is NaN.  Every score of a row with an infinite
+// element is infinite or NaN, so its softmax is NaN; the factor of its scores says so, or scores of -inf alone would pass
+// for a row without keys.
+__device__ __forceinline__ __half2 add_unless_finite(uint32_t w, __half2 z) {
+    return __hfma2(*reinterpret_cast<const __half2 *>(&w), __float2half2_rn(0.0f), z);
+}
+
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * WARPS) : "memory"); }
 
 // Query fragments (the 8-column operand) of row g of each tile: 16 neighbouring elements of
 // chunk 2 c + i (D = 128) or c (D = 64) per i, as fp16.  bf16 rows are lifted by a power of two
 // to fp16's upper range, exact for every element above 2^-28 of the row's largest; the return
-// value takes it back.
+// value takes it back (NaN for a row that is not finite).
 template <typename TQ, int D>
 __device__ __forceinline__ float load_query(const Args &A, const Cursor &cur, int row, uint32_t (&qf)[D / 16][2]) {
     const int lane = threadIdx.x & 31, c = lane & 3;
@@ -321,12 +328,22 @@ __device__ __forceinline__ float load_query(const Args &A, const Cursor &cur, in
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const int e = min(max((int)(top >> 7) - 127, -100), 126);        // 2^e <= largest < 2^(e + 1)
         const float f = pow2(14 - e);
-        unscale = pow2(e - 14);
+        unscale = top < 0x7f80u ? pow2(e - 14) : NAN;
 #pragma unroll
         for (int k = 0; k < NI; ++k)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 w[k][j] = pack_f16(__uint_as_float(w[k][j] << 16) * f, __uint_as_float(w[k][j] & 0xffff0000u) * f);
+    } else {
+        __half2 z = __float2half2_rn(0.0f);
+#pragma unroll
+        for (int k = 0; k < NI; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) z = add_unless_finite(w[k][j], z);
+        unscale += __low2float(z) + __high2float(z);
+        unscale += __shfl_xor_sync(0xffffffffu, unscale, 1);               // of the four lanes that hold the row
+        unscale += __shfl_xor_sync(0xffffffffu, unscale, 2);
+        unscale *= 0.25f;
     }
 #pragma unroll
     for (int k = 0; k < NI; ++k)

@@ -41,6 +41,7 @@ namespace awq {
 namespace kv {
 namespace pre {
 
+using dec::add_unless_finite;
 using dec::cvt_hi;
 using dec::cvt_lo;
 using dec::ex2;
@@ -323,7 +324,7 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                         }
                         const int e = min(max((int)(top >> 7) - 127, -100), 126);
                         const float f = pow2(14 - e);
-                        rowf *= pow2(e - 14);
+                        rowf *= top < 0x7f80u ? pow2(e - 14) : NAN;
 #pragma unroll
                         for (int i = 0; i < D / 8; ++i) {
                             uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
@@ -332,6 +333,12 @@ kv_prefill_kernel(const __grid_constant__ CUtensorMap tmap_k, const __grid_const
                                 x[k] = pack_f16(__uint_as_float(x[k] << 16) * f, __uint_as_float(x[k] & 0xffff0000u) * f);
                             v[i] = make_uint4(x[0], x[1], x[2], x[3]);
                         }
+                    } else {
+                        __half2 z = __float2half2_rn(0.0f);
+#pragma unroll
+                        for (int i = 0; i < D / 8; ++i)
+                            z = add_unless_finite(v[i].x, add_unless_finite(v[i].y, add_unless_finite(v[i].z, add_unless_finite(v[i].w, z))));
+                        rowf += __low2float(z) + __high2float(z);
                     }
                     const uint32_t dst = smem_u32(sm + S::OFF_Q + t * S::OPERAND);
 #pragma unroll

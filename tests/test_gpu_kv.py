@@ -938,3 +938,18 @@ def test_senseless_offsets_and_lengths_touch_nothing_else(awq, cu, lens):
         awq.get_status()
     except awq.AWQError as e:
         assert e.code == 1
+
+
+@pytest.mark.parametrize("D,dtype", [(128, F16), (64, BF16), (64, F16)])
+@pytest.mark.parametrize("lens,new,H,G,extra", NAN_CASES)
+def test_attention_of_infinite_queries(awq, lens, new, H, G, extra, D, dtype):
+    """An infinite element makes every score of its row infinite or NaN, so the row is NaN -- also where all scores are
+    -inf: channels whose keys have one sign are common."""
+    c, q, lens, cu, pages = _attend_case(300 + len(lens) + G, lens, new, H, G, D, 32)
+    pages = np.concatenate([pages, np.full((len(lens), extra), 1 << 30, np.int32)], 1)
+    codes = c["k_codes"][..., 7]
+    codes[codes != 127] &= 127                                             # this channel's keys: none below zero, none zero
+    codes[codes == 0] = 1
+    q[::2, 0, 7], q[1::3, -1, 7], q[-1, (H * G) // 2, 7] = -np.inf, np.inf, -np.inf
+    with np.errstate(invalid="ignore"):                                    # the oracle's inf - inf
+        _close_but_nan(*_attend(awq, c, q, lens, cu, pages, dtype, D), dtype, D)
