@@ -360,9 +360,11 @@ __global__ void __launch_bounds__(128, 8) rope_kernel(const RopeArgs A) {
 // warps of four rows of keys and values each, which stay in registers, so k and v are
 // read once, the block's exponents are known before any code is written, and no two teams
 // touch the same block; one warp and one row where every sequence has one new token.
-// Bound by the bytes of k, v and q; in decode by latency.  Seven prompts, 8 + 32 heads,
-// 345 MB: 87 us on the device (4.0 TB/s), 119 with the queries rotated after the appends;
-// 256 single tokens, 8 + 64 heads: 6.5 us; one: 3.6.
+// Seven prompts, 8 + 32 heads, 345 MB: 87 us on the device (4.0 TB/s), 119 with the queries
+// rotated after the appends; 256 single tokens, 8 + 64 heads: 6.5 us; one: 3.6.  The prompts are
+// bound by instructions beside waits for loads: 61 % of the issue slots and 45 % of the ALUs,
+// HBM at 44 %, 22 warps an SM that wait for their rows longer than for anything else (nothing of
+// a team's next item is on its way meanwhile).  Decode is latency: lengths, page, rows, old scale.
 // Rows are dealt to blocks of threads in chunks: the rows of a chunk that open a
 // block (its leaders) are found by a ballot, and (leader, head) items go round the teams.
 // Other blocks of threads of the same launch rotate the queries.

@@ -254,9 +254,12 @@ cudaError_t launch_decode_rows(awq::kv::dec::Args &A, int sms,
     e = launch_overlapped(kernel, dim3(grid), awq::kv::dec::THREADS, S::BYTES, st, mk, mv, (const awq::kv::dec::Args)A);
     if (e != cudaSuccess) return e;
     constexpr int W = awq::kv::dec::JOIN_WARPS;
-    // Dim 64: the join is launched plainly.  Launched early it slows the calls around it down (32 heads of 64, window 2048,
-    // replayed back to back: 24 sequences 56 us a call, 41 plainly; 12: 33 and 27; 6: 24 and 18; why, the counters of a kernel
-    // by itself do not show).  Dim 128: an early start saves 1 to 2 us (131072 keys, calls in a row: 53.3 us, 55.0 plainly).
+    // Dim 64: the join is launched plainly, dim 128: early.  Calls in a row, early and plainly (us): dim 64, 24 / 12 / 6
+    // sequences of 32 heads of their own, window 2048: 58, 34, 24 and 43, 29, 20.5; 64 x 64 heads over 8, to 8192 keys: 69 and
+    // 57; 24 and 6 x 32 over 8: 29.5, 18.6 and 30.8, 19.4.  Dim 128: the same three of own heads: 65, 38, 24.3 and 65, 39.5,
+    // 26; 64 x 64 over 8: 96.8 and 98.4; 32 over 8: 44.6, 18.5 and 46.4, 20.4; 131072 keys: 52.9 and 53.8; but 24 x 32 own heads
+    // of 2048 keys: 79 and 74.6.  The dimension stands for what it mostly goes with, and no more; why an early start can cost
+    // that much, the counters of a kernel by itself do not show.
     const dim3 joins = A.by_segment ? dim3((unsigned)segments, rows) : dim3(grid, (rows + W - 1) / W);
     auto join = A.by_segment ? awq::kv::dec::kv_decode_join_kernel<TQ, D, W> : awq::kv::dec::kv_decode_join_kernel<TQ, D, 1>;
     if (D == 128) return launch_overlapped(join, joins, 32 * W, 0, st, (const awq::kv::dec::Args)A);

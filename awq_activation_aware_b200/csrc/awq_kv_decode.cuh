@@ -43,9 +43,11 @@
 //    (all their elements become NaN; elsewhere only those that the product reaches).
 //  * Measured (us on the device): 131072 keys of 8 heads, dim 128: 52 with 8 rows a
 //    head, 56 with 16, 88 with 32 (floor 41); 524288 keys 173, 6.2 TB/s; 64 sequences
-//    of 4096 keys 94, 5.75 TB/s; 516 keys 9.6.  About 12 us of a long call do not grow
+//    of 4096 keys 94, 5.75 TB/s; 516 keys 9.7.  About 12 us of a long call do not grow
 //    with the keys: lengths, page numbers and keys come one after another, and the
-//    join.  Dim 64 and 17 to 32 rows are bound by instructions, not by HBM.
+//    join.  Dim 64 and 17 to 32 rows are bound by instructions, not by HBM.  With dim
+//    128 the forms of 16 and 32 rows spill 104 bytes a thread at 168 registers,
+//    that of 8 rows 16 to 20 at 128; those of dim 64 none.
 #pragma once
 
 #include <type_traits>

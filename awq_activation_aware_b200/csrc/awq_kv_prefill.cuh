@@ -28,11 +28,16 @@
 // With too few blocks of rows to fill the machine the keys are split over several
 // blocks of threads, and a second kernel joins their parts in order.
 //
-// Measured (device): 8192 new tokens, 32 query heads over 8, dim 128: 625 us, 879
-// TFLOP/s (dim 64: 516 us, 533); 512 tokens after 16000, 64 heads: 290 us, 941 TFLOP/s.
-// What bounds it is the softmax beside the products: two warps a scheduler take 2350
-// clocks for 128 scores of a row by themselves and 2720 with the products running,
-// whose operands come through the same shared memory.
+// Measured (device, graphs of ten calls on one input): 8192 new tokens, 32 query heads
+// over 8, dim 128: 624 us, 881 TFLOP/s (dim 64: 516 us, 533); 512 tokens after 16000, 64
+// heads: 289 us, 943 TFLOP/s.  No single unit bounds it.  256 rows x 128 keys take 4800
+// clocks, of which the tensor pipe is busy for 2670 (56 %; its operations alone are 2048:
+// a product of 64 keys takes 49 clocks for 32, because it reads 128 rows of Q for 64 of K),
+// shared memory for 3380 wavefronts (1024 Q, 1024 K and V, 1080 loads and stores, 256 TMA),
+// the special functions 46 % and the ALUs 36 %.  The softmax of two warps a scheduler takes
+// 2350 clocks by itself, 2720 with products beside.  What is left over is waiting: scores,
+// softmax and products of a tile come one after the other, and two tiles and two score
+// buffers do not cover all of it.
 #pragma once
 
 #include "awq_kv_decode.cuh"
