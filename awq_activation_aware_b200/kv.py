@@ -411,6 +411,11 @@ def attention_step(x: torch.Tensor, qkv: dict, o: dict, cache: dict, seq_lens: t
     if qkv["codes"].shape[0] != (q_heads + 2 * heads) * D:
         raise ValueError(f"qkv has {qkv['codes'].shape[0]} rows, {q_heads} + 2 x {heads} heads of {D} need "
                          f"{(q_heads + 2 * heads) * D}")
+    # what the attention would refuse, before the tokens are appended
+    if q_heads < 1 or q_heads % heads:
+        raise ValueError(f"{q_heads} query heads are not a multiple of the cache's {heads}")
+    if window < 0 or not 1 <= max_tokens <= _MAX or (cu_tokens is None and max_tokens != 1):
+        raise ValueError(f"window must be at least 0 and max_tokens 1 or more (1 without cu_tokens), got {window} and {max_tokens}")
     if x.dim() != 2:
         raise ValueError("x must be [tokens, hidden]")
     T, hidden = x.shape

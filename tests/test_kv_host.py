@@ -343,3 +343,24 @@ def test_status_is_read_on_the_streams_device(monkeypatch):
     with pytest.raises(awq.AWQError):
         awq.get_status(_Stream(1))
     assert asked == [0, 1]
+
+
+def test_a_step_is_refused_before_it_appends(monkeypatch):
+    """What the attention would refuse, the step refuses first: the cache keeps its state."""
+    done = []
+    monkeypatch.setattr(awq, "qlinear", lambda codes, *a, **k: done.append("qlinear") or torch.zeros((3, codes.shape[0])))
+    monkeypatch.setattr(awq.kv, "_cuda", lambda t, name: -1)
+    monkeypatch.setattr(awq.kv, "_on", lambda *a: awq.kv._HERE)
+    monkeypatch.setattr(awq.kv, "kv_append", lambda *a, q=None, **k: done.append("append") or q)
+    cache = awq.kv_cache(2, 2, 16, 64, device="cpu")
+    x, table, cu = torch.zeros((3, 256), dtype=torch.float16), torch.zeros(1), torch.zeros(1)
+
+    def call(q_heads, **kw):
+        awq.attention_step(x, _packed_layer((q_heads + 4) * 64, 256, 4, 128), _packed_layer(320, q_heads * 64, 4, 64) |
+                           dict(bits=4, group_size=64), cache, None, None, table, q_heads, **kw)
+
+    for bad in (dict(q_heads=3), dict(q_heads=0), dict(q_heads=4, window=-1), dict(q_heads=4, max_tokens=0, cu_tokens=cu),
+                dict(q_heads=4, max_tokens=2), dict(q_heads=4, max_tokens=1 << 31, cu_tokens=cu)):
+        with pytest.raises(ValueError):
+            call(**bad)
+    assert not done
