@@ -953,3 +953,66 @@ def test_attention_of_infinite_queries(awq, lens, new, H, G, extra, D, dtype):
     q[::2, 0, 7], q[1::3, -1, 7], q[-1, (H * G) // 2, 7] = -np.inf, np.inf, -np.inf
     with np.errstate(invalid="ignore"):                                    # the oracle's inf - inf
         _close_but_nan(*_attend(awq, c, q, lens, cu, pages, dtype, D), dtype, D)
+
+
+def _step_of(awq, HQ, H, D, hidden, seed):
+    """Random packed layers of an attention block: Q, K and V stacked, and the output projection."""
+    from awq_activation_aware_b200 import synth
+    out = []
+    for i, (N, K) in enumerate((((HQ + 2 * H) * D, hidden), (hidden, HQ * D))):
+        W, X, _ = synth.generate(synth.make_config(N, K, 256, bits=4, group=128, seed=seed + i))
+        out.append(awq.quantize_layer(dev(W), dev(X)))
+    return out
+
+
+@pytest.mark.parametrize("new", [[1, 1], [3, 2], [40, 9]])
+def test_attention_step_of_a_padded_batch(awq, new):
+    """Rows behind the last sequence may hold anything: no other row, and no byte of the cache, depends on them."""
+    HQ, H, D, hidden = 4, 2, 64, 256
+    qkv, o = _step_of(awq, HQ, H, D, hidden, 11)
+    T, pad, lens = sum(new), 5, [new[0] + 20, new[1]]
+    pages, table, cu = ints([[1, 0, 4], [3, 2, 5]]), awq.rope_table(96, D), ints([0, new[0], T])
+    x = torch.randn((T + pad, hidden), device="cuda").half()
+    base, got = _upload(_random_cache(np.random.default_rng(12), 6, H, 32, D)), []
+    for fill in (0.0, float("nan"), 6e4):
+        x[T:] = fill
+        cache = {k: t.clone() for k, t in base.items()}
+        y = awq.attention_step(x, qkv, o, cache, ints(lens), pages, table, HQ, cu, max(new))
+        got.append([y[:T]] + [t.view(torch.uint8) if t.dtype != F32 else t for t in cache.values()])
+    awq.get_status()
+    assert bool(torch.isfinite(got[0][0]).all())
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+@pytest.mark.parametrize("new", [None, [6, 0, 2]])
+def test_a_captured_attention_step_follows_its_inputs(awq, new):
+    """The whole step captured once, replayed as the sequences grow, equal to the step called each time."""
+    HQ, H, D, hidden = 4, 2, 64, 256
+    qkv, o = _step_of(awq, HQ, H, D, hidden, 13)
+    T, most = (3, 1) if new is None else (sum(new), max(new))
+    cu = None if new is None else ints(np.concatenate([[0], np.cumsum(new)]))
+    pages, table = ints(np.random.default_rng(14).permutation(12).reshape(3, 4)), awq.rope_table(128, D)
+    base = _random_cache(np.random.default_rng(15), 12, H, 32, D)
+    live, ref = _upload(base), _upload(base)
+    x, lens = torch.randn((T, hidden), device="cuda").half(), ints([30, 9, 64])
+    step = lambda cache: awq.attention_step(x, qkv, o, cache, lens, pages, table, HQ, cu, most)  # noqa: E731
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step(_upload(base))                                                # kernels are loaded before the capture
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            out = step(live)
+    torch.cuda.synchronize()
+    for i in range(4):
+        x.copy_(torch.randn_like(x) * (i + 1))
+        lens += most
+        g.replay()
+        torch.cuda.synchronize()
+        got = out.clone()
+        assert torch.equal(got, step(ref))
+        for k in live:
+            a, b = (t[k].view(torch.uint8) if k.endswith("codes") else t[k] for t in (live, ref))
+            assert torch.equal(a, b)
+    awq.get_status()
