@@ -514,8 +514,10 @@ AWQ_API awq_status awq_kv_append(awq_kv_cache cache, awq_kv_batch batch, int64_t
  *   lse         float [T, q.heads] or NULL: ln sum_j exp(scale q . k_j)
  *   ws          ws_bytes >= awq_kv_attention_workspace_bytes(...), 256-byte aligned;
  *               overwritten by every call: calls that share it must be ordered
- * A NaN code reaches the rows that see its key, and no others; a NaN or an infinity in a row of
- * q makes that row of out and lse NaN, unless it sees no key.  A NaN score is NaN in lse, too.
+ * A NaN code reaches the rows that see its key, and no others: of a key, the whole row and its
+ * lse; of a value, at least its element, and all of the row with its lse where some row of the
+ * same tile does not see the key.  A NaN or an infinity in a row of q makes that row of out and
+ * lse NaN, unless it sees no key.
  * Sequences have at most 2^30 tokens.  Make a first call of a kind before a stream capture: it
  * loads the kernel.
  * Bases 16-byte aligned, strides multiples of 8 elements; out may not overlap q. */
