@@ -515,8 +515,8 @@ AWQ_API awq_status awq_kv_append(awq_kv_cache cache, awq_kv_batch batch, int64_t
  *   ws          ws_bytes >= awq_kv_attention_workspace_bytes(...), 256-byte aligned;
  *               overwritten by every call: calls that share it must be ordered
  * A NaN code reaches the rows that see its key, and no others: of a key, the whole row and its
- * lse; of a value, at least its element, and all of the row with its lse where some row of the
- * same tile does not see the key.  A NaN or an infinity in a row of q makes that row of out and
+ * lse; of a value, at least its element, and all of the row with its lse where the tile of keys
+ * around it is not full or not seen by every row.  A NaN or an infinity in a row of q makes that row of out and
  * lse NaN, unless it sees no key.
  * Sequences have at most 2^30 tokens.  Make a first call of a kind before a stream capture: it
  * loads the kernel.
